@@ -80,6 +80,16 @@ def load():
                   L.nvfp4_qad_kl, L.nvfp4_gemm, L.nvfp4_gemm_bf16, L.nvfp4_gemm_quantize_x, L.nvfp4_amax_quantize,
                   L.nvfp4_amax_fakequant):
             f.restype = i32
+        f32, f64, u32 = ctypes.c_float, ctypes.c_double, ctypes.c_uint32
+        L.nvfp4_layer_norm.argtypes = [vp, i32, vp, vp, i32, i64, i64, f32, vp, vp, vp, vp, vp]
+        L.nvfp4_layer_norm_backward.argtypes = [vp, vp, i32, vp, i32, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp]
+        L.nvfp4_tensor_plan.argtypes = [vp, i64, vp, i64, vp]
+        L.nvfp4_grad_norm.argtypes = [vp, i64, f32, vp, vp, vp, vp]
+        L.nvfp4_adamw.argtypes = [vp, i64, vp, f32, vp, f64, f64, f32, u32, vp, vp, i64, vp]
+        for f in (L.nvfp4_layer_norm, L.nvfp4_layer_norm_backward, L.nvfp4_tensor_plan, L.nvfp4_grad_norm, L.nvfp4_adamw):
+            f.restype = i32
+        L.nvfp4_layer_norm_workspace.argtypes, L.nvfp4_layer_norm_workspace.restype = [i64, i64], i64
+        L.nvfp4_tensor_plan_bytes.argtypes, L.nvfp4_tensor_plan_bytes.restype = [vp, i64], i64
         L.nvfp4_status_string.argtypes, L.nvfp4_status_string.restype = [i32], ctypes.c_char_p
         L.nvfp4_version.argtypes, L.nvfp4_version.restype = [], i32
         _lib = L
@@ -412,3 +422,9 @@ def fakequant_ste(x, mode="four_over_six", rule="mse", groups: int = 1, amax_val
             return g
 
     return _FakeQuantSTE.apply(x)
+
+
+from . import train as _train  # noqa: E402  (the operators of nvfp4_train.h)
+from .train import *  # noqa: E402,F401,F403
+
+__all__ += _train.__all__

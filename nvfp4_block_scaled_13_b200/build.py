@@ -2,7 +2,7 @@
 
     python -m nvfp4_block_scaled_13_b200.build [--force]
 
-The library is a plain C-ABI shared object (include/nvfp4.h) with the CUDA runtime linked
+The library is a plain C-ABI shared object (include/nvfp4.h, include/nvfp4_train.h) with the CUDA runtime linked
 statically; it is written next to this file under lib/ so it travels with the source tree.
 """
 from __future__ import annotations
@@ -35,7 +35,7 @@ def sources():
 
 def deps():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(ROOT, "include", "nvfp4.h"), __file__]
+        os.path.join(ROOT, "include", "nvfp4.h"), os.path.join(ROOT, "include", "nvfp4_train.h"), __file__]
 
 
 def up_to_date() -> bool:

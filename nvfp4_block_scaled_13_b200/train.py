@@ -1,0 +1,393 @@
+"""Binding of include/nvfp4_train.h: the operators of a quantization-aware-distillation step
+around ``fakequant_ste`` and ``qad_kl``: layer norm (forward with the amax of its result, and
+backward), the global gradient norm with its clip factor, and AdamW over many tensors at once
+with the states in 32 bits or in 8.
+
+``nvfp4_*`` mirror the C ABI one to one; the wrappers allocate with torch and check shapes,
+types and devices. Tensors are CUDA, contiguous and on one device, which need not be the current
+one; the work goes to ``stream``, or to the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import functools
+import math
+from typing import NamedTuple
+
+from . import _check, _ptr, _stream, load
+
+__all__ = [
+    "TYPE_BF16", "TYPE_F32", "OptTensor", "nvfp4_layer_norm", "nvfp4_layer_norm_workspace",
+    "nvfp4_layer_norm_backward", "nvfp4_tensor_plan_bytes", "nvfp4_tensor_plan", "nvfp4_grad_norm", "nvfp4_adamw",
+    "Normed", "layer_norm", "layer_norm_forward", "layer_norm_backward",
+    "GradientList", "AdamWPlan", "gradient_list", "adamw_plan", "grad_norm", "adamw",
+]
+
+TYPE_BF16, TYPE_F32 = 0, 1
+_GRAD_NORM_WORKSPACE = 16400
+_STATE_ALIGN = 128      # elements: a tensor's states start on a multiple of it
+
+
+class OptTensor(ctypes.Structure):
+    """nvfp4_opt_tensor."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("numel", ctypes.c_int64), ("first", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32)]
+
+
+# ---- the C ABI, one to one -------------------------------------------------------------------
+
+def nvfp4_layer_norm(x, x_type, weight, bias, w_type, rows, cols, eps, y, mean=None, rstd=None, amax=None, stream=None):
+    _check(load().nvfp4_layer_norm(_ptr(x), x_type, _ptr(weight), _ptr(bias), w_type, rows, cols, eps, _ptr(y),
+                                   _ptr(mean), _ptr(rstd), _ptr(amax), _stream(stream)), "nvfp4_layer_norm")
+
+
+def nvfp4_layer_norm_workspace(rows, cols) -> int:
+    return load().nvfp4_layer_norm_workspace(rows, cols)
+
+
+def nvfp4_layer_norm_backward(dy, x, x_type, weight, w_type, mean, rstd, rows, cols, dx, dweight=None, dbias=None,
+                              workspace=None, workspace_bytes=0, stream=None):
+    _check(load().nvfp4_layer_norm_backward(_ptr(dy), _ptr(x), x_type, _ptr(weight), w_type, _ptr(mean), _ptr(rstd),
+                                            rows, cols, _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                            workspace_bytes, _stream(stream)), "nvfp4_layer_norm_backward")
+
+
+def nvfp4_tensor_plan_bytes(tensors, count) -> int:
+    return load().nvfp4_tensor_plan_bytes(tensors, count)
+
+
+def nvfp4_tensor_plan(tensors, count, image, image_bytes) -> int:
+    """Writes the plan to host memory and returns the number of chunks."""
+    chunks = ctypes.c_int64()
+    _check(load().nvfp4_tensor_plan(tensors, count, image, image_bytes, ctypes.byref(chunks)), "nvfp4_tensor_plan")
+    return chunks.value
+
+
+def nvfp4_grad_norm(plan, chunks, max_norm, norm, scale, workspace, stream=None):
+    _check(load().nvfp4_grad_norm(_ptr(plan), chunks, max_norm, _ptr(norm), _ptr(scale), _ptr(workspace),
+                                  _stream(stream)), "nvfp4_grad_norm")
+
+
+def nvfp4_adamw(plan, chunks, control, lr, lr_device, beta1, beta2, eps, seed, scale=None, amax=None, count=0,
+                stream=None):
+    _check(load().nvfp4_adamw(_ptr(plan), chunks, _ptr(control), lr, _ptr(lr_device), beta1, beta2, eps, seed,
+                              _ptr(scale), _ptr(amax), count, _stream(stream)), "nvfp4_adamw")
+
+
+# ---- checks shared by the wrappers ---------------------------------------------------------------
+
+def _type_of(t, what):
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return TYPE_BF16
+    if t.dtype == torch.float32:
+        return TYPE_F32
+    raise ValueError(f"nvfp4: {what} must be BF16 or FP32, not {t.dtype}")
+
+
+def _on(device):
+    """A context in which `device` is current."""
+    import torch
+
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _lend(stream, *tensors):
+    """Memory that torch's current stream allocated and `stream` works on is kept until that work is done."""
+    import torch
+
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(tensors[0].device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=tensors[0].device)
+    if stream.cuda_stream != current.cuda_stream:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _rows_cols(x, what):
+    if not x.is_cuda:
+        raise ValueError("nvfp4: tensors must live on a CUDA device")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{what}: x must have a last dimension of at least 1")
+    cols = x.shape[-1]
+    return x.numel() // cols, cols
+
+
+def _same(t, x, shape, what, dtype=None):
+    if t.device != x.device:
+        raise ValueError(f"nvfp4: {what} must be on {x.device}, not {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"nvfp4: {what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"nvfp4: {what} must be {dtype}, not {t.dtype}")
+
+
+# ---- layer norm ----------------------------------------------------------------------------------
+
+class Normed(NamedTuple):
+    y: "object"       # as x
+    mean: "object"    # float32 [rows] or None
+    rstd: "object"    # float32 [rows] or None
+    amax: "object"    # float32 [1] or None: max |y|, the amax of y's quantization
+
+
+def _affine(x, weight, bias, cols):
+    """The type of weight and bias, which agree."""
+    given = [(t, name) for t, name in ((weight, "weight"), (bias, "bias")) if t is not None]
+    for t, name in given:
+        _same(t, x, (cols,), name, given[0][0].dtype)
+    return _type_of(*given[0]) if given else TYPE_F32
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, with_stats=True, with_amax=False,
+                       stream=None) -> Normed:
+    """Layer norm of BF16 or FP32 x over its last dimension; weight and bias (BF16 or FP32, [cols])
+    may be None. ``with_stats`` returns what the backward pass needs, ``with_amax`` the amax of
+    y, ready for ``quantize`` and ``quantize_for_gemm``. No autograd: see ``layer_norm``."""
+    import torch
+
+    rows, cols = _rows_cols(x, "layer_norm")
+    x_type, w_type = _type_of(x, "x"), _affine(x, weight, bias, cols)
+    with _on(x.device):
+        y = torch.empty_like(x)
+        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device) if with_stats else None
+        mean, rstd = (stats[0], stats[1]) if with_stats else (None, None)
+        top = torch.empty(1, dtype=torch.float32, device=x.device) if with_amax else None
+        nvfp4_layer_norm(x, x_type, weight, bias, w_type, rows, cols, eps, y, mean, rstd, top, stream)
+        _lend(stream, *(t for t in (y, stats, top) if t is not None))
+    return Normed(y, mean, rstd, top)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, with_weight=True, with_bias=True, stream=None):
+    """(dx, dweight, dbias) of layer norm from its input and the statistics of its forward pass.
+    dweight and dbias have the weight's type (FP32 without one); None where not asked for."""
+    import torch
+
+    rows, cols = _rows_cols(x, "layer_norm_backward")
+    _same(dy, x, x.shape, "dy", x.dtype)
+    _same(mean, x, (rows,), "mean", torch.float32)
+    _same(rstd, x, (rows,), "rstd", torch.float32)
+    x_type, w_type = _type_of(x, "x"), _affine(x, weight, None, cols)
+    with _on(x.device):
+        dx = torch.empty_like(x)
+        grads = [torch.empty(cols, dtype=torch.float32 if weight is None else weight.dtype, device=x.device) if asked
+                 else None for asked in (with_weight, with_bias)]
+        size = nvfp4_layer_norm_workspace(rows, cols) if with_weight or with_bias else 0
+        work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+        nvfp4_layer_norm_backward(dy, x, x_type, weight, w_type, mean, rstd, rows, cols, dx, *grads, work, size, stream)
+        _lend(stream, *(t for t in (dx, *grads, work) if t is not None))
+    return dx, grads[0], grads[1]
+
+
+@functools.lru_cache(maxsize=None)
+def _layer_norm_function():
+    import torch
+
+    class _LayerNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, eps, with_amax):
+            r = layer_norm_forward(x, weight, bias, eps, True, with_amax)
+            ctx.save_for_backward(x, weight, r.mean, r.rstd)
+            ctx.bias_dtype = None if bias is None else bias.dtype
+            if not with_amax:
+                return r.y
+            ctx.mark_non_differentiable(r.amax)
+            return r.y, r.amax
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy, *_):
+            x, weight, mean, rstd = ctx.saved_tensors
+            needs = ctx.needs_input_grad
+            dx, dweight, dbias = layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, needs[1], needs[2])
+            if dbias is not None:
+                dbias = dbias.to(ctx.bias_dtype)
+            return dx if needs[0] else None, dweight, dbias, None, None
+
+    return _LayerNorm
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, with_amax=False):
+    """y, or (y, amax): layer norm with autograd through x, weight and bias. The amax [1] is that
+    of y's quantization (``fakequant_ste(y, amax_values=amax)``, ``quantize_for_gemm``)."""
+    import torch
+
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+        return _layer_norm_function().apply(x, weight, bias, eps, with_amax)
+    r = layer_norm_forward(x, weight, bias, eps, False, with_amax)
+    return (r.y, r.amax) if with_amax else r.y
+
+
+# ---- lists of tensors ------------------------------------------------------------------------------
+
+class GradientList:
+    """Gradients whose norm ``grad_norm`` takes: their table on the device, and the kernel's
+    scratch. The tensors are the ones given: write new gradients into them. Calls with one list
+    must not overlap on the GPU."""
+
+    def __init__(self, grads, device, records):
+        import torch
+
+        self.grads, self.device, self.count = grads, device, len(records)
+        array = (OptTensor * max(1, len(records)))(*records)
+        size = nvfp4_tensor_plan_bytes(array, len(records))
+        if size < 0:
+            raise ValueError("nvfp4: too many tensors or elements in one list")
+        image = torch.empty(size, dtype=torch.uint8)
+        self.chunks = nvfp4_tensor_plan(array, len(records), image.data_ptr(), size)
+        self.table = image.to(device)
+        self.work = torch.zeros(_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=device)
+
+
+class AdamWPlan(GradientList):
+    """Parameters, gradients and AdamW states of one list (see ``adamw_plan``).
+
+    ``exp_avg``, ``exp_avg_sq`` (and ``master``, ``exp_avg_scale``, ``exp_avg_sq_scale``) are flat
+    buffers; those of tensor i start at ``offsets[i]`` (scales at ``offsets[i] // 32``), and
+    ``state(i)`` gives them as views. With 8-bit states ``exp_avg_sq`` holds codes of the second
+    moment's root. ``amax`` [count] is written by every ``adamw`` (None without ``with_amax``)."""
+
+    def steps(self) -> int:
+        """Steps taken so far (waits for the GPU)."""
+        return int(self.control[4].item())
+
+    def set_steps(self, steps: int):
+        """Sets the count of steps, as after loading the states of a checkpoint."""
+        self.control.copy_(_control(steps, self.betas))
+
+    def state(self, i: int) -> dict:
+        at, n = self.offsets[i], self.numels[i]
+        out = {"exp_avg": self.exp_avg[at:at + n], "exp_avg_sq": self.exp_avg_sq[at:at + n]}
+        if self.master is not None:
+            out["master"] = self.master[at:at + n]
+        if self.state_bits == 8:
+            blocks = slice(at // 32, at // 32 + (n + 31) // 32)
+            out["exp_avg_scale"], out["exp_avg_sq_scale"] = self.exp_avg_scale[blocks], self.exp_avg_sq_scale[blocks]
+        return out
+
+
+def _control(steps, betas):
+    """nvfp4_adamw_control after `steps` steps, as 8 words on the host."""
+    import torch
+
+    if not 0 <= steps < 1 << 32:
+        raise ValueError("nvfp4: the number of steps must be in [0, 2^32)")
+    powers = torch.tensor([betas[0] ** steps, betas[1] ** steps], dtype=torch.float64).view(torch.int32)
+    count = torch.tensor([steps - (1 << 32) if steps >= 1 << 31 else steps, 0, 0, 0], dtype=torch.int32)
+    return torch.cat([powers, count])
+
+
+def _list_of(tensors, what):
+    tensors = list(tensors)
+    if not tensors or not sum(t.numel() for t in tensors):
+        raise ValueError(f"nvfp4: {what} are empty")
+    for t in tensors:
+        if t.device != tensors[0].device:
+            raise ValueError(f"nvfp4: {what} must be on one device")
+        _ptr(t)   # CUDA and contiguous
+    return tensors
+
+
+def gradient_list(grads) -> GradientList:
+    """A list of BF16 or FP32 gradients for ``grad_norm``."""
+    grads = _list_of(grads, "grads")
+    with _on(grads[0].device):
+        return GradientList(grads, grads[0].device,
+                            [OptTensor(grad=g.data_ptr(), numel=g.numel(), grad_type=_type_of(g, "a gradient")) for g in grads])
+
+
+def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=0.01, betas=(0.9, 0.999),
+               eps: float = 1e-8, seed: int = 0, step: int = 0, with_amax=False) -> AdamWPlan:
+    """AdamW over `params` (BF16 or FP32) with the gradients in `grads`, which keep their memory
+    from step to step (assign them to ``p.grad`` and clear them in place).
+
+    ``state_bits``: 32, or 8 (E4M3 with a power-of-two scale for each 32 elements). ``masters``: an
+    FP32 master of every BF16 parameter; without one a BF16 parameter is rounded stochastically.
+    ``weight_decay``: one number, or one for each tensor. ``seed`` (32 bits) of the stochastic
+    rounding. ``step``: steps taken before. States start at zero, masters at the parameters."""
+    import torch
+
+    params, grads = _list_of(params, "params"), _list_of(grads, "grads")
+    if len(params) != len(grads):
+        raise ValueError("adamw_plan: one gradient for each parameter")
+    decays = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
+    if len(decays) != len(params):
+        raise ValueError("adamw_plan: one weight decay, or one for each parameter")
+    if state_bits not in (32, 8):
+        raise ValueError("adamw_plan: state_bits must be 32 or 8")
+    if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1) or not 0 <= eps < math.inf or not 0 <= seed < 1 << 32:
+        raise ValueError("adamw_plan: betas must be in [0, 1), eps finite and >= 0, seed in [0, 2^32)")
+    device = params[0].device
+    offsets, total = [], 0
+    for p, g in zip(params, grads):
+        _same(g, p, p.shape, "a gradient")
+        offsets.append(total)
+        total += -(-p.numel() // _STATE_ALIGN) * _STATE_ALIGN
+    flat = {}
+    with _on(device), torch.no_grad():
+        master = torch.zeros(total, dtype=torch.float32, device=device) if masters else None
+        for name in ("exp_avg", "exp_avg_sq"):
+            if state_bits == 32:
+                flat[name] = torch.zeros(total, dtype=torch.float32, device=device)
+            else:
+                flat[name] = torch.zeros(total, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                flat[name + "_scale"] = torch.ones(total // 32, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
+        records = []
+        for p, g, at, decay in zip(params, grads, offsets, decays):
+            record = OptTensor(param=p.data_ptr(), grad=g.data_ptr(), numel=p.numel(), first=at, weight_decay=decay,
+                               param_type=_type_of(p, "a parameter"), grad_type=_type_of(g, "a gradient"), state_bits=state_bits)
+            if masters and p.dtype == torch.bfloat16:
+                master[at:at + p.numel()].copy_(p.detach().reshape(-1))
+                record.master = master.data_ptr() + 4 * at
+            for name in ("exp_avg", "exp_avg_sq"):
+                setattr(record, name, flat[name].data_ptr() + at * flat[name].element_size())
+                if state_bits == 8:
+                    setattr(record, name + "_scale", flat[name + "_scale"].data_ptr() + at // 32)
+            records.append(record)
+        plan = AdamWPlan(grads, device, records)
+        plan.params, plan.offsets, plan.numels = params, offsets, [p.numel() for p in params]
+        plan.state_bits, plan.betas, plan.eps, plan.seed = state_bits, (float(betas[0]), float(betas[1])), float(eps), seed
+        plan.master, plan.exp_avg, plan.exp_avg_sq = master, flat["exp_avg"], flat["exp_avg_sq"]
+        plan.exp_avg_scale, plan.exp_avg_sq_scale = flat.get("exp_avg_scale"), flat.get("exp_avg_sq_scale")
+        plan.control = _control(step, plan.betas).to(device)
+        plan.amax = torch.zeros(len(params), dtype=torch.float32, device=device) if with_amax else None
+    return plan
+
+
+def grad_norm(grads: GradientList, max_norm: float = math.inf, stream=None):
+    """(norm, scale), each [1] on the device: the norm of all gradients of the list together and
+    min(1, max_norm / (norm + 1e-6)). A norm that is not finite gives a NaN scale, with which
+    ``adamw`` leaves everything as it is."""
+    import torch
+
+    with _on(grads.device):
+        out = torch.empty((2, 1), dtype=torch.float32, device=grads.device)
+        nvfp4_grad_norm(grads.table, grads.chunks, max_norm, out[0], out[1], grads.work, stream)
+        _lend(stream, out)
+    return out[0], out[1]
+
+
+def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
+    """One AdamW step, in place. ``lr``: a number, or an FP32 [1] tensor that the kernel reads (a
+    captured call then follows it; the count of steps is kept on the device anyway). ``scale``:
+    an FP32 [1] factor of the gradients, as ``grad_norm`` gives it."""
+    import torch
+
+    if not isinstance(plan, AdamWPlan):
+        raise ValueError("adamw: needs a plan of adamw_plan")
+    lr_device = None
+    if isinstance(lr, torch.Tensor):
+        _same(lr, plan.control, (1,), "lr", torch.float32)
+        lr, lr_device = 0.0, lr
+    if scale is not None:
+        _same(scale, plan.control, (1,), "scale", torch.float32)
+    with _on(plan.device):
+        nvfp4_adamw(plan.table, plan.chunks, plan.control, lr, lr_device, plan.betas[0], plan.betas[1], plan.eps, plan.seed,
+                    scale, plan.amax, plan.count if plan.amax is not None else 0, stream)
