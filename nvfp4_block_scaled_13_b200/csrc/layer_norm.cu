@@ -5,8 +5,8 @@
 // dx = rstd (h - S h / C - xh S(h xh) / C), dw = S_rows dy xh, db = S_rows dy.
 // Both are bound by memory: 4 bytes an element forward and 6 backward in BF16.
 //
-// A row belongs to a group of threads: 8, 16 or 32 lanes of a warp (no barrier), or a CTA. A
-// thread holds its share of the row in registers from the loads to the result, so x (and dy) are
+// A row belongs to a group of threads: 8, 16 or 32 lanes of a warp (no barrier), a CTA, or, over
+// 8192 columns, a cluster of CTAs that exchange their sums through shared memory. A thread holds its share of the row in registers from the loads to the result, so x (and dy) are
 // read once, and holds its columns' weight and bias (and their gradients' sums) over all the rows
 // that its group works through. The variance is summed from the held row after the mean is
 // known: no cancellation, at the price of a second reduction.
@@ -95,10 +95,13 @@ __device__ __forceinline__ void join_top(uint32_t& top, const uint4& w, float) {
 __device__ __forceinline__ uint32_t top_bits(uint32_t top, bf16) { return max(top << 16, top & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t top_bits(uint32_t top, float) { return top; }
 
-__device__ __forceinline__ void copy_async(uint4* to, const void* from) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))),
-                 "l"(from)
-                 : "memory");
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 read_shared(uint32_t from) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+    return v;
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -133,24 +136,42 @@ __device__ __forceinline__ void keep(float2 (&v)[H], uint32_t mask) {
     }
 }
 
-// Starts the copy of one unit of a tensor of `total` elements. A unit that reaches over the
-// tensor's ends (only where the tensor itself is not aligned) is copied by the element.
-template <typename T, bool SHIFTED>
-__device__ __forceinline__ void fetch_unit(uint4* slot, const T* tensor, int64_t at, int64_t total, uint32_t mask) {
-    constexpr int E = kUnit<T>;
-    if (mask == 0) return;
-    if (SHIFTED && (at < 0 || at + E > total)) {
-        T* to = reinterpret_cast<T*>(slot);
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (mask >> j & 1u) to[j] = tensor[at + j];
-    } else {
-        copy_async(slot, tensor + at);
+// A row operand as one thread sees it: the address of its unit 0 in the row that comes next. A
+// unit that reaches over the tensor's ends (only where the tensor itself is not aligned) is copied
+// by the element.
+template <typename T, int Q, bool SHIFTED>
+struct Source {
+    const char *next, *begin, *end;
+
+    __device__ __forceinline__ Source(const void* tensor, int64_t rows, int64_t first, const Columns<T, Q, SHIFTED>& at)
+        : begin(static_cast<const char*>(tensor)), end(begin + rows * at.cols * int64_t(sizeof(T))) {
+        next = begin + (first * at.cols + at.start(0)) * int64_t(sizeof(T));
     }
-}
+    __device__ __forceinline__ void fetch(int q, uint32_t unit_bytes, uint32_t slot, uint32_t mask) const {
+        constexpr int E = kUnit<T>;
+        const char* from = next + q * unit_bytes;
+        if (mask == Columns<T, Q, SHIFTED>::kAll) {
+            copy_async(slot, from);
+        } else if (SHIFTED && mask) {
+            if (from >= begin && from + 16 <= end) {
+                copy_async(slot, from);
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    if (!(mask >> j & 1u)) continue;
+                    if (E == 8) {
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(slot + 2 * j), "h"(reinterpret_cast<const uint16_t*>(from)[j]) : "memory");
+                    } else {
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 4 * j), "r"(reinterpret_cast<const uint32_t*>(from)[j]) : "memory");
+                    }
+                }
+            }
+        }
+    }
+};
 
 template <typename T>
-__device__ __forceinline__ void store_unit(T* to, const uint4& w, uint32_t mask) {
+__device__ __forceinline__ void store_unit(void* to, const uint4& w, uint32_t mask) {
     constexpr int E = kUnit<T>;
     if (mask == (1u << E) - 1u) {
         *reinterpret_cast<uint4*>(to) = w;
@@ -203,28 +224,68 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, bool vector,
 template <int LANES>
 __device__ __forceinline__ float lane_sum(float v) {
 #pragma unroll
-    for (int off = (LANES ? LANES : 32) / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    for (int off = (LANES > 0 ? LANES : 32) / 2; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
     return v;
 }
 
-// Partial sums of a CTA's warps, two sets that alternate: the barrier of the next reduction
-// separates this one's reads from the writes after next, so a reduction has one barrier.
+// LANES of a row that a CTA has, or a cluster of CTAs.
+constexpr int kCta = 0, kCluster = -1;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Partial sums of the warps of a row, in two sets that alternate: the barrier of the next
+// reduction separates this one's reads from the writes after next, so a reduction has one
+// barrier. In a cluster every warp leaves its sum in the shared memory of every CTA.
+template <int LANES>
 struct WarpSums {
-    float4 set[2][4];   // 16 warps
+    static constexpr int kFours = LANES == kCluster ? 32 : 4;   // 8 CTAs of 16 warps, or 16 warps
+    float4 set[2][kFours];
+
     __device__ __forceinline__ void clear() {
-        if (threadIdx.x < 8) (&set[0][0])[threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = threadIdx.x; k < 2 * kFours; k += blockDim.x) (&set[0][0])[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     __device__ __forceinline__ void put(int which, float v) {
-        if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(set[which])[threadIdx.x >> 5] = v;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        float* to = reinterpret_cast<float*>(set[which]);
+        if (LANES == kCluster) {
+            if (lane < static_cast<int>(cluster_size())) {
+                const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to + cluster_rank() * (blockDim.x >> 5) + warp));
+                uint32_t remote;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(lane));
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
+            }
+        } else if (lane == 0) {
+            to[warp] = v;
+        }
+    }
+    __device__ __forceinline__ void sync() const {
+        if (LANES == kCluster) {
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ float four(int which, int k) const {
+        const float4 p = set[which][k];
+        return (p.x + p.y) + (p.z + p.w);
     }
     __device__ __forceinline__ float total(int which) const {
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k * 128 >= blockDim.x) break;
-            const float4 p = set[which][k];
-            s += (p.x + p.y) + (p.z + p.w);
-        }
+        if (LANES == kCluster) return warp_sum(four(which, threadIdx.x & 31));
+        float s = four(which, 0);
+        if (blockDim.x > 128) s += four(which, 1);
+        if (blockDim.x > 256) s += four(which, 2 % kFours) + four(which, 3 % kFours);
         return s;
     }
 };
@@ -250,110 +311,149 @@ __device__ __forceinline__ void publish_amax(uint32_t top, uint32_t* amax) {
 
 // ---- forward -------------------------------------------------------------------------------
 
-// Rows in the ring; the longest FP32 rows have room for three.
-__host__ __device__ constexpr int forward_stages(int row_bytes_of_thread) { return row_bytes_of_thread > 64 ? 3 : 4; }
-constexpr int kBackwardStages = 3;
+constexpr int kForwardStages = 4, kBackwardStages = 3;   // rows in the ring
 
-// Registers of a thread, and with them the CTAs that an SM holds.
-constexpr int forward_registers(int elements) { return elements == 32 ? 128 : elements == 16 ? 80 : 64; }
+// Registers of a thread, and with them the CTAs that an SM holds (each of its four quarters has
+// 16384 registers).
+constexpr int forward_registers(int elements) { return elements == 16 ? 80 : 64; }
 constexpr int backward_registers(int elements) { return elements == 16 ? 128 : 80; }
-constexpr int resident(int registers, int threads) { return std::max(1, std::min(32, 65536 / registers / threads)); }
+constexpr int resident(int registers, int threads) {
+    return std::max(1, std::min(32, 16384 / (registers * 32) * 4 / (threads / 32)));
+}
 
-// N elements a thread; LANES threads a row, 0: the CTA.
+// Which rows a thread's group takes, and the shift that they share.
+template <typename T, int LANES, bool SHIFTED>
+struct Group {
+    int lanes, t, groups, index;
+    int64_t first, step;
+    int turns, rows;   // turns of the CTA's loop (the shuffles need every lane of a warp), rows of the group
+    int shift;
+    int part;          // index of the CTA, or cluster, and of its partial row
+
+    __device__ __forceinline__ Group(const void* x, int64_t all_rows, int cols) {
+        constexpr unsigned L = LANES > 0 ? LANES : 1;
+        int64_t base = blockIdx.x, ctas = gridDim.x;
+        lanes = LANES > 0 ? LANES : blockDim.x;
+        t = LANES > 0 ? threadIdx.x % L : threadIdx.x;
+        groups = LANES > 0 ? blockDim.x / L : 1;
+        index = LANES > 0 ? threadIdx.x / L : 0;
+        if (LANES == kCluster) {
+            const int size = static_cast<int>(cluster_size());
+            t += static_cast<int>(cluster_rank() * blockDim.x);
+            lanes *= size;
+            base /= size;
+            ctas /= size;
+        }
+        part = static_cast<int>(base);
+        base *= groups;
+        first = base + index;
+        step = ctas * groups;
+        turns = static_cast<int>((all_rows - base + step - 1) / step);
+        rows = first < all_rows ? static_cast<int>((all_rows - first + step - 1) / step) : 0;
+        shift = SHIFTED ? static_cast<int>(((reinterpret_cast<uintptr_t>(x) + first * cols * int64_t(sizeof(T))) & 15) / sizeof(T)) : 0;
+    }
+};
+
+// N elements a thread; LANES threads a row, or kCta, or kCluster.
 template <typename T, int N, int LANES, bool SHIFTED>
-__global__ void __maxnreg__(forward_registers(N)) norm_kernel(const NormArgs a) {
-    constexpr int E = kUnit<T>, Q = N / E, H = E / 2, S = forward_stages(N * sizeof(T));
+__global__ void __maxnreg__(forward_registers(N)) norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int E = kUnit<T>, Q = N / E, H = E / 2, S = kForwardStages;
+    constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
     extern __shared__ uint4 ring[];   // [S][Q][threads]
-    __shared__ WarpSums warp_sums;
-    const int threads = blockDim.x, lanes = LANES ? LANES : threads;
-    const int t = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
-    const int groups = LANES ? threads / (LANES ? LANES : 1) : 1;
-    const int64_t first = int64_t(blockIdx.x) * groups + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
-    const int64_t step = int64_t(gridDim.x) * groups, total = a.rows * a.cols;
-    const T* x = static_cast<const T*>(a.x);
-    const int shift = SHIFTED ? static_cast<int>((reinterpret_cast<uintptr_t>(x + first * a.cols) & 15) / sizeof(T)) : 0;
-    const Columns<T, Q, SHIFTED> at(t, lanes, shift, a.cols);
+    __shared__ WarpSums<LANES> warp_sums;
+    const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols);
+    const Columns<T, Q, SHIFTED> at(group.t, group.lanes, group.shift, a.cols);
     uint32_t mask[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) mask[q] = at.mask(q);
-
-    const auto fetch = [&](int64_t row, int stage) {
-        if (row < a.rows) {
+    const uint32_t unit_bytes = group.lanes * 16u, slot_bytes = blockDim.x * 16u;
+    const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
+    const uint32_t slots_end = slots + S * Q * slot_bytes;
+    const int64_t row_bytes = group.step * a.cols * int64_t(sizeof(T));
+    Source<T, Q, SHIFTED> x(a.x, a.rows, group.first, at);
+    int ahead = 0;   // rows whose copy has been started
+    const auto fetch = [&](uint32_t slot) {
+        if (ahead < group.rows) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
-                fetch_unit<T, SHIFTED>(&ring[(stage * Q + q) * threads + threadIdx.x], x, row * a.cols + at.start(q), total, mask[q]);
+            for (int q = 0; q < Q; ++q) x.fetch(q, unit_bytes, slot + q * slot_bytes, mask[q]);
         }
+        ++ahead;
+        x.next += row_bytes;
         commit_copies();
     };
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) fetch(first + s * step, s);
+    for (int s = 0; s < S - 1; ++s) fetch(slots + s * Q * slot_bytes);
     float2 w[Q][H], b[Q][H];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), mask[q], 1.0f, w[q]);
         load_param<E>(a.bias, a.w_f32, a.w_vector, at.start(q), mask[q], 0.0f, b[q]);
     }
-    if (!LANES) {
+    if (LANES <= 0) {
         warp_sums.clear();
-        __syncthreads();
+        warp_sums.sync();
     }
-    const float inv = 1.0f / static_cast<float>(a.cols);
+    const float inv = 1.0f / static_cast<float>(a.cols), eps = a.eps;
+    char* y = static_cast<char*>(a.y) + (group.first * a.cols + at.start(0)) * int64_t(sizeof(T));
+    const bool stats = group.t == 0 && (a.mean || a.rstd), tops = a.amax;
     uint32_t top = 0;
-    int stage = 0;
-    // Every lane of a warp makes the same number of turns: the shuffles need them all.
-    const int64_t turns = LANES ? (a.rows - int64_t(blockIdx.x) * groups + step - 1) / step : (a.rows - first + step - 1) / step;
-    int64_t r = first;
-    for (int64_t turn = 0; turn < turns; ++turn, r += step) {
+    uint32_t slot = slots, refill = slots + (S - 1) * Q * slot_bytes;
+    for (int turn = 0; turn < group.turns; ++turn) {
         wait_copies<S - 2>();
         float2 v[Q][H];
-        float2 sum2 = make_float2(0.0f, 0.0f);
+        float2 sum2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            unpack(ring[(stage * Q + q) * threads + threadIdx.x], v[q], T{});
-            if (mask[q] != Columns<T, Q, SHIFTED>::kAll) keep(v[q], mask[q]);
+            unpack(read_shared(slot + q * slot_bytes), v[q], T{});
+            if (mask[q] != kAll) keep(v[q], mask[q]);
 #pragma unroll
-            for (int k = 0; k < H; ++k) sum2 = add2(sum2, v[q][k]);
+            for (int k = 0; k < H; ++k) sum2[k & 1] = add2(sum2[k & 1], v[q][k]);
         }
-        fetch(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
-        stage = stage == S - 1 ? 0 : stage + 1;
-        float sum = lane_sum<LANES>(sum2.x + sum2.y);
-        if (!LANES) {
+        fetch(refill);
+        refill = slot;
+        slot += Q * slot_bytes;
+        if (slot == slots_end) slot = slots;
+        sum2[0] = add2(sum2[0], sum2[1]);
+        float sum = lane_sum<LANES>(sum2[0].x + sum2[0].y);
+        if (LANES <= 0) {
             warp_sums.put(0, sum);
-            __syncthreads();
+            warp_sums.sync();
             sum = warp_sums.total(0);
         }
         const float mean = sum * inv;
-        float2 square2 = make_float2(0.0f, 0.0f);
+        float2 square2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
 #pragma unroll
             for (int k = 0; k < H; ++k) v[q][k] = add2(v[q][k], make_float2(-mean, -mean));
-            if (mask[q] != Columns<T, Q, SHIFTED>::kAll) keep(v[q], mask[q]);
+            if (mask[q] != kAll) keep(v[q], mask[q]);
 #pragma unroll
-            for (int k = 0; k < H; ++k) square2 = fma2(v[q][k], v[q][k], square2);
+            for (int k = 0; k < H; ++k) square2[k & 1] = fma2(v[q][k], v[q][k], square2[k & 1]);
         }
-        float square = lane_sum<LANES>(square2.x + square2.y);
-        if (!LANES) {
+        square2[0] = add2(square2[0], square2[1]);
+        float square = lane_sum<LANES>(square2[0].x + square2[0].y);
+        if (LANES <= 0) {
             warp_sums.put(1, square);
-            __syncthreads();
+            warp_sums.sync();
             square = warp_sums.total(1);
         }
-        const float rstd = rsqrtf(fmaf(square, inv, a.eps));
-        if (r < a.rows) {
-            T* y = static_cast<T*>(a.y) + r * a.cols;
+        const float rstd = rsqrtf(fmaf(square, inv, eps));
+        if (LANES <= 0 || turn < group.rows) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
 #pragma unroll
                 for (int k = 0; k < H; ++k) v[q][k] = fma2(mul2(v[q][k], make_float2(rstd, rstd)), w[q][k], b[q][k]);
                 const uint4 out = pack(v[q], T{});
-                if (a.amax && mask[q]) join_top(top, out, T{});
-                store_unit(y + at.start(q), out, mask[q]);
+                if (tops) join_top(top, out, T{});   // columns that do not exist hold zero
+                store_unit<T>(y + q * unit_bytes, out, mask[q]);
             }
-            if (t == 0) {
+            if (stats) {
+                const int64_t r = group.first + turn * group.step;
                 if (a.mean) a.mean[r] = mean;
                 if (a.rstd) a.rstd[r] = rstd;
             }
         }
+        y += row_bytes;
     }
     wait_copies<0>();
     if (a.amax) publish_amax(top_bits(top, T{}), a.amax);
@@ -436,38 +536,55 @@ __device__ __forceinline__ void join_groups(const float2 (&s)[Q][kUnit<T> / 2], 
     __syncthreads();
 }
 
+// A unit's column sums; `vector` where the partial rows lie as the operands' rows do.
+template <int E>
+__device__ __forceinline__ void store_sums(float* to, const float2 (&s)[E / 2], uint32_t mask, bool vector) {
+    if (vector) {
+        if (mask) {
+#pragma unroll
+            for (int k = 0; k < E / 4; ++k)
+                reinterpret_cast<float4*>(to)[k] = make_float4(s[2 * k].x, s[2 * k].y, s[2 * k + 1].x, s[2 * k + 1].y);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if (mask >> j & 1u) to[j] = j & 1 ? s[j / 2].y : s[j / 2].x;
+    }
+}
+
 template <typename T, int N, int LANES, bool SHIFTED>
-__global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const NormGradArgs a) {
+__global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     constexpr int E = kUnit<T>, Q = N / E, H = E / 2, S = kBackwardStages;
-    extern __shared__ uint4 ring[];   // [S][x, dy][Q][threads]
-    __shared__ WarpSums sums1, sums2;
-    __shared__ float joined[LANES ? LANES * N : 1];
-    const int threads = blockDim.x, lanes = LANES ? LANES : threads;
-    const int t = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
-    const int groups = LANES ? threads / (LANES ? LANES : 1) : 1, group = LANES ? threadIdx.x / (LANES ? LANES : 1) : 0;
-    const int64_t first = int64_t(blockIdx.x) * groups + group;
-    const int64_t step = int64_t(gridDim.x) * groups, total = a.rows * a.cols;
-    const T* x = static_cast<const T*>(a.x);
-    const T* dy = static_cast<const T*>(a.dy);
-    const int shift = SHIFTED ? static_cast<int>((reinterpret_cast<uintptr_t>(x + first * a.cols) & 15) / sizeof(T)) : 0;
-    const Columns<T, Q, SHIFTED> at(t, lanes, shift, a.cols);
+    constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
+    extern __shared__ uint4 ring[];   // [S][Q][x, dy][threads]
+    __shared__ WarpSums<LANES> sums1, sums2;
+    __shared__ float joined[LANES > 0 ? LANES * N : 1];
+    const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols);
+    const Columns<T, Q, SHIFTED> at(group.t, group.lanes, group.shift, a.cols);
     uint32_t mask[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) mask[q] = at.mask(q);
-
-    const auto fetch = [&](int64_t row, int stage) {
-        if (row < a.rows) {
+    const uint32_t unit_bytes = group.lanes * 16u, slot_bytes = blockDim.x * 16u;
+    const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
+    const uint32_t slots_end = slots + S * Q * 2 * slot_bytes;
+    const int64_t row_bytes = group.step * a.cols * int64_t(sizeof(T));
+    Source<T, Q, SHIFTED> x(a.x, a.rows, group.first, at), dy(a.dy, a.rows, group.first, at);
+    int ahead = 0;
+    const auto fetch = [&](uint32_t slot) {
+        if (ahead < group.rows) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                const int64_t place = row * a.cols + at.start(q);
-                fetch_unit<T, SHIFTED>(&ring[((stage * 2) * Q + q) * threads + threadIdx.x], x, place, total, mask[q]);
-                fetch_unit<T, SHIFTED>(&ring[((stage * 2 + 1) * Q + q) * threads + threadIdx.x], dy, place, total, mask[q]);
+                x.fetch(q, unit_bytes, slot + 2 * q * slot_bytes, mask[q]);
+                dy.fetch(q, unit_bytes, slot + (2 * q + 1) * slot_bytes, mask[q]);
             }
         }
+        ++ahead;
+        x.next += row_bytes;
+        dy.next += row_bytes;
         commit_copies();
     };
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) fetch(first + s * step, s);
+    for (int s = 0; s < S - 1; ++s) fetch(slots + s * Q * 2 * slot_bytes);
     float2 w[Q][H], sw[Q][H], sb[Q][H];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -475,32 +592,35 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const NormGr
 #pragma unroll
         for (int k = 0; k < H; ++k) sw[q][k] = sb[q][k] = make_float2(0.0f, 0.0f);
     }
-    if (!LANES) {
+    if (LANES <= 0) {
         sums1.clear();
         sums2.clear();
-        __syncthreads();
+        sums1.sync();
     }
     const float inv = 1.0f / static_cast<float>(a.cols);
-    int stage = 0, which = 0;
-    const int64_t turns = LANES ? (a.rows - int64_t(blockIdx.x) * groups + step - 1) / step : (a.rows - first + step - 1) / step;
-    int64_t r = first;
-    float next_mean = r < a.rows ? a.mean[r] : 0.0f, next_rstd = r < a.rows ? a.rstd[r] : 0.0f;
-    for (int64_t turn = 0; turn < turns; ++turn, r += step) {
+    char* dx = static_cast<char*>(a.dx) + (group.first * a.cols + at.start(0)) * int64_t(sizeof(T));
+    const float *means = a.mean + group.first, *rstds = a.rstd + group.first;
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (group.rows > 0) {
+        next_mean = *means;
+        next_rstd = *rstds;
+    }
+    uint32_t slot = slots, refill = slots + (S - 1) * Q * 2 * slot_bytes;
+    for (int turn = 0; turn < group.turns; ++turn) {
         const float mean = next_mean, rstd = next_rstd;
-        const bool exists = r < a.rows;   // a group past the last row adds nothing
+        const bool exists = LANES <= 0 || turn < group.rows;   // a group past its last row adds nothing
         wait_copies<S - 2>();
         float2 xh[Q][H], h[Q][H];
         float2 s1 = make_float2(0.0f, 0.0f), s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            unpack(ring[((stage * 2) * Q + q) * threads + threadIdx.x], xh[q], T{});
-            unpack(ring[((stage * 2 + 1) * Q + q) * threads + threadIdx.x], h[q], T{});
-            const uint32_t m = exists ? mask[q] : 0u;
+            unpack(read_shared(slot + 2 * q * slot_bytes), xh[q], T{});
+            unpack(read_shared(slot + (2 * q + 1) * slot_bytes), h[q], T{});
 #pragma unroll
             for (int k = 0; k < H; ++k) xh[q][k] = mul2(add2(xh[q][k], make_float2(-mean, -mean)), make_float2(rstd, rstd));
-            if (m != Columns<T, Q, SHIFTED>::kAll) {
-                keep(xh[q], m);
-                keep(h[q], m);
+            if (mask[q] != kAll || !exists) {
+                keep(xh[q], exists ? mask[q] : 0u);
+                keep(h[q], exists ? mask[q] : 0u);
             }
 #pragma unroll
             for (int k = 0; k < H; ++k) {
@@ -511,50 +631,50 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const NormGr
                 s2 = fma2(h[q][k], xh[q][k], s2);
             }
         }
-        fetch(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
-        stage = stage == S - 1 ? 0 : stage + 1;
-        if (r + step < a.rows) {
-            next_mean = a.mean[r + step];
-            next_rstd = a.rstd[r + step];
+        fetch(refill);
+        refill = slot;
+        slot += Q * 2 * slot_bytes;
+        if (slot == slots_end) slot = slots;
+        means += group.step;
+        rstds += group.step;
+        if (turn + 1 < group.rows) {
+            next_mean = *means;
+            next_rstd = *rstds;
         }
         float t1 = lane_sum<LANES>(s1.x + s1.y), t2 = lane_sum<LANES>(s2.x + s2.y);
-        if (!LANES) {
-            sums1.put(which, t1);
-            sums2.put(which, t2);
-            __syncthreads();
-            t1 = sums1.total(which);
-            t2 = sums2.total(which);
-            which ^= 1;
+        if (LANES <= 0) {
+            sums1.put(turn & 1, t1);
+            sums2.put(turn & 1, t2);
+            sums1.sync();
+            t1 = sums1.total(turn & 1);
+            t2 = sums2.total(turn & 1);
         }
-        t1 *= inv;
-        t2 *= inv;
+        t1 *= -inv;
+        t2 *= -inv;
         if (exists) {
-            T* dx = static_cast<T*>(a.dx) + r * a.cols;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
 #pragma unroll
                 for (int k = 0; k < H; ++k)
-                    h[q][k] = mul2(add2(h[q][k], fma2(xh[q][k], make_float2(-t2, -t2), make_float2(-t1, -t1))), make_float2(rstd, rstd));
-                store_unit(dx + at.start(q), pack(h[q], T{}), mask[q]);
+                    h[q][k] = mul2(add2(h[q][k], fma2(xh[q][k], make_float2(t2, t2), make_float2(t1, t1))), make_float2(rstd, rstd));
+                store_unit<T>(dx + q * unit_bytes, pack(h[q], T{}), mask[q]);
             }
         }
+        dx += row_bytes;
     }
     wait_copies<0>();
     if (a.sums) {
-        float* out = a.sums + int64_t(blockIdx.x) * a.cols;
+        float* out = a.sums + int64_t(group.part) * a.cols;
         float* out_b = out + int64_t(a.parts) * a.cols;
-        if (LANES) {
-            join_groups<T, Q, SHIFTED>(sw, at, group, groups, joined, out);
-            join_groups<T, Q, SHIFTED>(sb, at, group, groups, joined, out_b);
+        if (LANES > 0) {
+            join_groups<T, Q, SHIFTED>(sw, at, group.index, group.groups, joined, out);
+            join_groups<T, Q, SHIFTED>(sb, at, group.index, group.groups, joined, out_b);
         } else {
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
-#pragma unroll
-                for (int j = 0; j < E; ++j)
-                    if (mask[q] >> j & 1u) {
-                        out[at.start(q) + j] = j & 1 ? sw[q][j / 2].y : sw[q][j / 2].x;
-                        out_b[at.start(q) + j] = j & 1 ? sb[q][j / 2].y : sb[q][j / 2].x;
-                    }
+            for (int q = 0; q < Q; ++q) {
+                store_sums<E>(out + at.start(q), sw[q], mask[q], !SHIFTED);
+                store_sums<E>(out_b + at.start(q), sb[q], mask[q], !SHIFTED);
+            }
         }
     }
 }
@@ -640,47 +760,66 @@ nvfp4_status launched() { return cudaGetLastError() == cudaSuccess ? NVFP4_OK : 
 // How rows are given to threads.
 struct Cut {
     int elements;   // of a thread; 0: by norm_long_kernel and its like
-    int lanes;      // of a row: 8, 16, 32, or 0 for a CTA
+    int lanes;      // of a row: 8, 16, 32, kCta or kCluster
     int threads;    // of a CTA
+    int cluster;    // CTAs of a row
     bool shifted;
 };
 
 // Rows that start on 16 bytes take whole units; others, where all operands' rows start at the same
 // place within 16 bytes, are shifted.
-Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent, int most_elements) {
+Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent) {
     const int unit = 16 / size;
     const bool shifted = !aligned || cols % unit != 0;
     const int64_t need = cols + (shifted ? unit - 1 : 0);
-    if (!congruent) return {0, 0, 0, false};
-    if (need <= 64) return {8, 8, 128, shifted};
-    if (need <= 128) return {8, 16, 128, shifted};
-    if (need <= 256) return {8, 32, 128, shifted};
-    if (need <= 512) return {16, 32, 128, shifted};
-    for (int elements = 16; elements <= most_elements; elements *= 2) {
-        const int64_t threads = (need + 32 * elements - 1) / (32 * elements) * 32;
-        if (threads <= 512) return {elements, 0, static_cast<int>(threads), shifted};
+    if (!congruent) return {0, 0, 0, 1, false};
+    if (need <= 64) return {8, 8, 128, 1, shifted};
+    if (need <= 128) return {8, 16, 128, 1, shifted};
+    if (need <= 256) return {8, 32, 128, 1, shifted};
+    if (need <= 512) return {16, 32, 128, 1, shifted};
+    for (int cluster = 1; cluster <= 8; cluster *= 2) {
+        const int64_t threads = (need + 512 * cluster - 1) / (512 * cluster) * 32;
+        if (threads <= 512) return {16, cluster == 1 ? kCta : kCluster, static_cast<int>(threads), cluster, shifted};
     }
-    return {0, 0, 0, false};
+    return {0, 0, 0, 1, false};
 }
 
-// CTAs that share the rows: at most `resident`, and so many that every group keeps its shift.
-int64_t grid_of(const Cut& cut, int64_t rows, int64_t resident, int size) {
-    const int64_t groups = cut.lanes ? cut.threads / cut.lanes : 1, need = (rows + groups - 1) / groups;
-    if (need <= resident) return need;
+// Groups of CTAs (one, or a cluster) that share the rows: at most the `resident` ones, and so many
+// that every row group keeps its shift.
+int64_t parts_of(const Cut& cut, int64_t rows, int64_t resident_ctas, int size) {
+    const int64_t groups = cut.lanes > 0 ? cut.threads / cut.lanes : 1, need = (rows + groups - 1) / groups;
+    const int64_t room = std::max<int64_t>(1, resident_ctas / cut.cluster);
+    if (need <= room) return need;
     const int64_t unit = 16 / size;
-    return resident * groups % unit == 0 ? resident : std::max<int64_t>(unit, resident / unit * unit);
+    return room * groups % unit == 0 ? room : std::max<int64_t>(unit, room / unit * unit);
 }
 
-Cut cut_backward(int64_t cols, int size, bool aligned, bool congruent) { return cut_rows(cols, size, aligned, congruent, 16); }
-
-// CTAs of the backward pass, each of which leaves a partial row.
+// Partial rows of the backward pass.
 int64_t backward_parts(const Cut& cut, int64_t rows, int64_t cols, int size) {
     const int64_t sms = sm_count();
     if (cut.elements == 0) {
         const int64_t across = (cols + 255) / 256;
         return std::min<int64_t>(rows, std::max<int64_t>(1, 4 * sms / across));
     }
-    return grid_of(cut, rows, sms * resident(backward_registers(cut.elements), cut.threads), size);
+    return parts_of(cut, rows, sms * resident(backward_registers(cut.elements), cut.threads), size);
+}
+
+// One CTA a part, or a cluster.
+template <typename Args>
+nvfp4_status launch_rows(void (*kernel)(const Args), const Args& a, int64_t parts, const Cut& cut, size_t smem, cudaStream_t stream) {
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(static_cast<unsigned>(parts * cut.cluster));
+    config.blockDim = dim3(cut.threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = stream;
+    cudaLaunchAttribute attribute{};
+    attribute.id = cudaLaunchAttributeClusterDimension;
+    attribute.val.clusterDim.x = cut.cluster;
+    attribute.val.clusterDim.y = attribute.val.clusterDim.z = 1;
+    config.attrs = &attribute;
+    config.numAttrs = cut.cluster > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, a);
+    return e == cudaSuccess ? launched() : (cudaGetLastError(), NVFP4_ERR_CUDA);
 }
 
 // Lets `kernel` have `bytes` of dynamic shared memory; without asking it may have 48 KiB with the
@@ -702,28 +841,30 @@ bool allow_smem(size_t bytes) {
     return true;
 }
 
-nvfp4_status clear_amax(uint32_t* amax, unsigned grid, cudaStream_t stream) {
+nvfp4_status clear_amax(uint32_t* amax, int64_t grid, cudaStream_t stream) {
     return amax && grid > 1 && cudaMemsetAsync(amax, 0, 4, stream) != cudaSuccess ? NVFP4_ERR_CUDA : NVFP4_OK;
 }
 
 template <typename T, int N, int LANES, bool SHIFTED>
 nvfp4_status launch_norm(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
     constexpr auto kernel = norm_kernel<T, N, LANES, SHIFTED>;
-    const size_t smem = size_t(forward_stages(N * sizeof(T))) * N * sizeof(T) * cut.threads;
+    const size_t smem = size_t(kForwardStages) * N * sizeof(T) * cut.threads;
     if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
-    const unsigned grid = static_cast<unsigned>(grid_of(cut, a.rows, int64_t(sm_count()) * resident(forward_registers(N), cut.threads), sizeof(T)));
-    if (clear_amax(a.amax, grid, stream) != NVFP4_OK) return NVFP4_ERR_CUDA;
-    kernel<<<grid, cut.threads, smem, stream>>>(a);
-    return launched();
+    const int64_t parts = parts_of(cut, a.rows, int64_t(sm_count()) * resident(forward_registers(N), cut.threads), sizeof(T));
+    if (clear_amax(a.amax, parts * cut.cluster, stream) != NVFP4_OK) return NVFP4_ERR_CUDA;
+    return launch_rows<NormArgs>(kernel, a, parts, cut, smem, stream);
 }
 
 template <typename T, bool SHIFTED>
 nvfp4_status dispatch_norm(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
-    if (cut.lanes == 8) return launch_norm<T, 8, 8, SHIFTED>(a, cut, stream);
-    if (cut.lanes == 16) return launch_norm<T, 8, 16, SHIFTED>(a, cut, stream);
-    if (cut.lanes == 32)
-        return cut.elements == 8 ? launch_norm<T, 8, 32, SHIFTED>(a, cut, stream) : launch_norm<T, 16, 32, SHIFTED>(a, cut, stream);
-    return cut.elements == 16 ? launch_norm<T, 16, 0, SHIFTED>(a, cut, stream) : launch_norm<T, 32, 0, SHIFTED>(a, cut, stream);
+    switch (cut.lanes) {
+        case 8: return launch_norm<T, 8, 8, SHIFTED>(a, cut, stream);
+        case 16: return launch_norm<T, 8, 16, SHIFTED>(a, cut, stream);
+        case 32:
+            return cut.elements == 8 ? launch_norm<T, 8, 32, SHIFTED>(a, cut, stream) : launch_norm<T, 16, 32, SHIFTED>(a, cut, stream);
+        case kCta: return launch_norm<T, 16, kCta, SHIFTED>(a, cut, stream);
+        default: return launch_norm<T, 16, kCluster, SHIFTED>(a, cut, stream);
+    }
 }
 
 unsigned long_threads(int64_t cols) { return static_cast<unsigned>(std::min<int64_t>(1024, (cols + 31) / 32 * 32)); }
@@ -744,17 +885,19 @@ nvfp4_status launch_grad(const NormGradArgs& a, const Cut& cut, cudaStream_t str
     constexpr auto kernel = norm_grad_kernel<T, N, LANES, SHIFTED>;
     const size_t smem = size_t(kBackwardStages) * 2 * N * sizeof(T) * cut.threads;
     if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
-    kernel<<<static_cast<unsigned>(a.parts), cut.threads, smem, stream>>>(a);
-    return launched();
+    return launch_rows<NormGradArgs>(kernel, a, a.parts, cut, smem, stream);
 }
 
 template <typename T, bool SHIFTED>
 nvfp4_status dispatch_grad(const NormGradArgs& a, const Cut& cut, cudaStream_t stream) {
-    if (cut.lanes == 8) return launch_grad<T, 8, 8, SHIFTED>(a, cut, stream);
-    if (cut.lanes == 16) return launch_grad<T, 8, 16, SHIFTED>(a, cut, stream);
-    if (cut.lanes == 32)
-        return cut.elements == 8 ? launch_grad<T, 8, 32, SHIFTED>(a, cut, stream) : launch_grad<T, 16, 32, SHIFTED>(a, cut, stream);
-    return launch_grad<T, 16, 0, SHIFTED>(a, cut, stream);
+    switch (cut.lanes) {
+        case 8: return launch_grad<T, 8, 8, SHIFTED>(a, cut, stream);
+        case 16: return launch_grad<T, 8, 16, SHIFTED>(a, cut, stream);
+        case 32:
+            return cut.elements == 8 ? launch_grad<T, 8, 32, SHIFTED>(a, cut, stream) : launch_grad<T, 16, 32, SHIFTED>(a, cut, stream);
+        case kCta: return launch_grad<T, 16, kCta, SHIFTED>(a, cut, stream);
+        default: return launch_grad<T, 16, kCluster, SHIFTED>(a, cut, stream);
+    }
 }
 
 template <typename T>
@@ -787,7 +930,7 @@ extern "C" nvfp4_status nvfp4_layer_norm(const void* x, nvfp4_type x_type, const
         if (amax && cudaMemsetAsync(amax, 0, 4, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
         return NVFP4_OK;
     }
-    const Cut cut = cut_rows(cols, type_size(x_type), place(x) == 0, place(x) == place(y), 32);
+    const Cut cut = cut_rows(cols, type_size(x_type), place(x) == 0, place(x) == place(y));
     const bool vector = !cut.shifted && place(weight) == 0 && place(bias) == 0;
     const NormArgs a{x, weight, bias, w_type == NVFP4_TYPE_F32, vector, rows, static_cast<int>(cols), eps, y, mean, rstd,
                      reinterpret_cast<uint32_t*>(amax)};
@@ -801,7 +944,7 @@ extern "C" int64_t nvfp4_layer_norm_workspace(int64_t rows, int64_t cols) {
     for (const int size : {2, 4})
         for (const bool aligned : {true, false})
             for (const bool congruent : {true, false})
-                parts = std::max(parts, backward_parts(cut_backward(cols, size, aligned, congruent), rows, cols, size));
+                parts = std::max(parts, backward_parts(cut_rows(cols, size, aligned, congruent), rows, cols, size));
     return 2 * parts * cols * 4;
 }
 
@@ -829,7 +972,7 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, const void* x,
     }
     if (sums && workspace_bytes < nvfp4_layer_norm_workspace(rows, cols)) return NVFP4_ERR_SHAPE;
     const int size = type_size(x_type);
-    const Cut cut = cut_backward(cols, size, place(x) == 0, place(x) == place(dy) && place(x) == place(dx));
+    const Cut cut = cut_rows(cols, size, place(x) == 0, place(x) == place(dy) && place(x) == place(dx));
     const bool vector = !cut.shifted && place(weight) == 0;
     const NormGradArgs a{dy, x, weight, w_type == NVFP4_TYPE_F32, vector, mean, rstd, rows, static_cast<int>(cols), dx,
                          sums ? static_cast<float*>(workspace) : nullptr, static_cast<int>(backward_parts(cut, rows, cols, size))};
