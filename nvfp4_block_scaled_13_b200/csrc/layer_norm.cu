@@ -86,8 +86,8 @@ __device__ __forceinline__ uint4 pack(const float2 (&v)[2], float) {
 
 // Running maximum of stored magnitudes: two BF16 halves, or one FP32 word.
 __device__ __forceinline__ void join_top(uint32_t& top, const uint4& w, bf16) {
-    top = __vmaxu2(__vmaxu2(top, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
-    top = __vmaxu2(__vmaxu2(top, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
+    for (const uint32_t v : {w.x, w.y, w.z, w.w})   // NaN stays
+        asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %1;\n\tmax.NaN.bf16x2 %0, %0, m;\n\t}" : "+r"(top) : "r"(v));
 }
 __device__ __forceinline__ void join_top(uint32_t& top, const uint4& w, float) {
     top = max(max(top, w.x & 0x7FFFFFFFu), max(w.y & 0x7FFFFFFFu, max(w.z & 0x7FFFFFFFu, w.w & 0x7FFFFFFFu)));
@@ -290,6 +290,11 @@ struct WarpSums {
     }
 };
 
+// Programmatic dependent launch: a kernel launched with it may start while its predecessor runs;
+// it waits for the predecessor's end before it touches what that wrote.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // One CTA alone writes its maximum; several join theirs with an (order-free) atomic maximum.
 __device__ __forceinline__ void publish_amax(uint32_t top, uint32_t* amax) {
     __shared__ uint32_t best[32];
@@ -303,6 +308,7 @@ __device__ __forceinline__ void publish_amax(uint32_t top, uint32_t* amax) {
             if (gridDim.x == 1) {
                 *amax = top;
             } else {
+                wait_for_previous();   // the kernel that clears it
                 atomicMax(amax, top);
             }
         }
@@ -356,7 +362,7 @@ struct Group {
 
 // N elements a thread; LANES threads a row, or kCta, or kCluster.
 template <typename T, int N, int LANES, bool SHIFTED>
-__global__ void __maxnreg__(forward_registers(N)) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid_constant__ NormArgs a) {
     constexpr int E = kUnit<T>, Q = N / E, H = E / 2, S = kForwardStages;
     constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
     extern __shared__ uint4 ring[];   // [S][Q][threads]
@@ -452,6 +458,124 @@ __global__ void __maxnreg__(forward_registers(N)) norm_kernel(const __grid_const
                 if (a.mean) a.mean[r] = mean;
                 if (a.rstd) a.rstd[r] = rstd;
             }
+        }
+        y += row_bytes;
+    }
+    wait_copies<0>();
+    if (a.amax) publish_amax(top_bits(top, T{}), a.amax);
+}
+
+// Rows of 257 to 8192 columns. With few elements a thread, the two reductions, the barriers and
+// the loop cost more instructions than the elements do and bound the kernel (measured at 8192 x
+// 4096 in BF16: 16.6 instructions an element and 29 us with 16 elements a thread). Here a row
+// belongs to WARPS warps with N elements a lane, one CTA of 16 warps has an SM to itself, and
+// weight and bias stay in its shared memory as binary32, so that registers hold nothing but the
+// row. The row groups of a CTA take every gridDim.x-th row, which gives all of them one shift.
+constexpr int kWideThreads = 512;
+
+template <typename T, int N, int WARPS, bool SHIFTED>
+__global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int E = kUnit<T>, Q = N / E, H = E / 2, P = E / 4, S = sizeof(T) == 2 ? 2 : 1;
+    constexpr int kUnits = WARPS * 32 * Q, kGroups = kWideThreads / 32 / WARPS;
+    constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll, kSlot = 512, kStage = Q * kSlot;
+    extern __shared__ uint4 ring[];   // rows [warp][S][Q][lane], then weight [P][kUnits], bias [P][kUnits]
+    __shared__ float sums[2][kGroups][WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / WARPS, t = (warp % WARPS) * 32 + lane;
+    float4* weights = reinterpret_cast<float4*>(ring + 16 * S * Q * 32);
+    float4* biases = weights + P * kUnits;
+    const uintptr_t place = reinterpret_cast<uintptr_t>(a.x) + blockIdx.x * (a.cols * uintptr_t(sizeof(T)));
+    const int shift = SHIFTED ? static_cast<int>((place & 15) / sizeof(T)) : 0;
+    const Columns<T, Q, SHIFTED> at(t, WARPS * 32, shift, a.cols);
+    const int64_t first = blockIdx.x + int64_t(group) * gridDim.x, step = int64_t(gridDim.x) * kGroups;
+    const int rows = first < a.rows ? static_cast<int>((a.rows - first + step - 1) / step) : 0;
+    const int64_t row_bytes = step * a.cols * int64_t(sizeof(T));
+    constexpr uint32_t kUnitBytes = WARPS * 512;
+
+    Source<T, Q, SHIFTED> x(a.x, a.rows, first, at);
+    const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * (S * kStage) + lane * 16u;
+    int ahead = 0;
+    const auto fetch = [&](uint32_t slot) {
+        if (ahead < rows) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) x.fetch(q, kUnitBytes, slot + q * kSlot, at.mask(q));
+        }
+        ++ahead;
+        x.next += row_bytes;
+        commit_copies();
+    };
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(slots + s * kStage);
+    for (int u = threadIdx.x; u < kUnits; u += kWideThreads) {
+        const Columns<T, 1, SHIFTED> one(u, 0, shift, a.cols);
+        float2 w[H], b[H];
+        load_param<E>(a.weight, a.w_f32, a.w_vector, one.start(0), one.mask(0), 1.0f, w);
+        load_param<E>(a.bias, a.w_f32, a.w_vector, one.start(0), one.mask(0), 0.0f, b);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            weights[p * kUnits + u] = make_float4(w[2 * p].x, w[2 * p].y, w[2 * p + 1].x, w[2 * p + 1].y);
+            biases[p * kUnits + u] = make_float4(b[2 * p].x, b[2 * p].y, b[2 * p + 1].x, b[2 * p + 1].y);
+        }
+    }
+    __syncthreads();
+    const float inv = 1.0f / static_cast<float>(a.cols), eps = a.eps;
+    char* y = static_cast<char*>(a.y) + (first * a.cols + at.start(0)) * int64_t(sizeof(T));
+    const bool stats = t == 0 && (a.mean || a.rstd), tops = a.amax;
+    // Sum over the row's warps; the two sets alternate as those of WarpSums do.
+    const auto row_sum = [&](float v, int which) {
+        v = warp_sum(v);
+        if (WARPS > 1) {
+            if (lane == 0) sums[which][group][warp % WARPS] = v;
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(WARPS * 32) : "memory");
+            v = sums[which][group][0];
+#pragma unroll
+            for (int k = 1; k < WARPS; ++k) v += sums[which][group][k];
+        }
+        return v;
+    };
+    uint32_t top = 0;
+    uint32_t slot = slots;
+    for (int turn = 0; turn < rows; ++turn) {
+        wait_copies<S - 1>();
+        float2 v[Q][H];
+        float2 part[4] = {};
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            unpack(read_shared(slot + q * kSlot), v[q], T{});
+            if (at.mask(q) != kAll) keep(v[q], at.mask(q));
+#pragma unroll
+            for (int k = 0; k < H; ++k) part[k % 4] = add2(part[k % 4], v[q][k]);
+        }
+        fetch(slot);
+        slot = S == 1 ? slot : slot == slots ? slots + kStage : slots;
+        part[0] = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+        const float mean = row_sum(part[0].x + part[0].y, 0) * inv;
+        float2 square[4] = {};
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+#pragma unroll
+            for (int k = 0; k < H; ++k) v[q][k] = add2(v[q][k], make_float2(-mean, -mean));
+            if (at.mask(q) != kAll) keep(v[q], at.mask(q));
+#pragma unroll
+            for (int k = 0; k < H; ++k) square[k % 4] = fma2(v[q][k], v[q][k], square[k % 4]);
+        }
+        square[0] = add2(add2(square[0], square[1]), add2(square[2], square[3]));
+        const float rstd = rsqrtf(fmaf(row_sum(square[0].x + square[0].y, 1), inv, eps));
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const float4 w = weights[p * kUnits + q * (WARPS * 32) + t], b = biases[p * kUnits + q * (WARPS * 32) + t];
+                v[q][2 * p] = fma2(mul2(v[q][2 * p], make_float2(rstd, rstd)), make_float2(w.x, w.y), make_float2(b.x, b.y));
+                v[q][2 * p + 1] = fma2(mul2(v[q][2 * p + 1], make_float2(rstd, rstd)), make_float2(w.z, w.w), make_float2(b.z, b.w));
+            }
+            const uint4 out = pack(v[q], T{});
+            if (tops) join_top(top, out, T{});   // columns that do not exist hold zero
+            store_unit<T>(y + q * kUnitBytes, out, at.mask(q));
+        }
+        if (stats) {
+            const int64_t r = first + turn * step;
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
         }
         y += row_bytes;
     }
@@ -557,6 +681,7 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
     constexpr int E = kUnit<T>, Q = N / E, H = E / 2, S = kBackwardStages;
     constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
     extern __shared__ uint4 ring[];   // [S][Q][x, dy][threads]
+    let_next_start();
     __shared__ WarpSums<LANES> sums1, sums2;
     __shared__ float joined[LANES > 0 ? LANES * N : 1];
     const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols);
@@ -725,25 +850,42 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const NormGradArgs a) {
     a.sums[int64_t(a.parts + blockIdx.y) * a.cols + c] = sb;
 }
 
-// Adds the partial rows: 32 columns a CTA, 8 threads a column, in a fixed order.
+// Adds the partial rows: 32 columns a CTA, 16 threads a column, in a fixed order. It is launched
+// while the kernel over the rows still runs and waits for its end here, which hides the launch.
+constexpr int kJoinWarps = 16;
+
 template <typename W>
-__global__ void __launch_bounds__(256) norm_join_kernel(const float* sums, int parts, int cols, W* dweight, W* dbias) {
-    __shared__ float shared[8][33];
+__global__ void __launch_bounds__(kJoinWarps * 32) norm_join_kernel(const float* sums, int parts, int cols, W* dweight, W* dbias) {
+    __shared__ float shared[kJoinWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     W* out = blockIdx.y == 0 ? dweight : dbias;
+    wait_for_previous();
     if (out == nullptr) return;
     const float* in = sums + int64_t(blockIdx.y) * parts * cols;
     float s = 0.0f;
-    if (c < cols)
-        for (int p = warp; p < parts; p += 8) s += in[int64_t(p) * cols + c];
+    if (c < cols) {
+        int p = warp;
+        for (; p + 7 * kJoinWarps < parts; p += 8 * kJoinWarps) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = in[int64_t(p + k * kJoinWarps) * cols + c];
+            s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+#pragma unroll 4
+        for (; p < parts; p += kJoinWarps) s += in[int64_t(p) * cols + c];
+    }
     shared[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < cols) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) s += shared[k][lane];
+        for (int k = 1; k < kJoinWarps; ++k) s += shared[k][lane];
         out[c] = from_float<W>(s);
     }
+}
+
+__global__ void clear_kernel(uint32_t* word) {
+    if (threadIdx.x == 0) *word = 0;
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -804,22 +946,34 @@ int64_t backward_parts(const Cut& cut, int64_t rows, int64_t cols, int size) {
     return parts_of(cut, rows, sms * resident(backward_registers(cut.elements), cut.threads), size);
 }
 
-// One CTA a part, or a cluster.
-template <typename Args>
-nvfp4_status launch_rows(void (*kernel)(const Args), const Args& a, int64_t parts, const Cut& cut, size_t smem, cudaStream_t stream) {
+// Launches a kernel with clusters of CTAs, and, where `after` is true, as one that may start
+// before its predecessor in the stream has ended.
+template <typename... Args>
+nvfp4_status launch(void (*kernel)(Args...), dim3 grid, int threads, int cluster, size_t smem, bool after, cudaStream_t stream,
+                    const Args&... args) {
     cudaLaunchConfig_t config{};
-    config.gridDim = dim3(static_cast<unsigned>(parts * cut.cluster));
-    config.blockDim = dim3(cut.threads);
+    config.gridDim = grid;
+    config.blockDim = dim3(threads);
     config.dynamicSmemBytes = smem;
     config.stream = stream;
-    cudaLaunchAttribute attribute{};
-    attribute.id = cudaLaunchAttributeClusterDimension;
-    attribute.val.clusterDim.x = cut.cluster;
-    attribute.val.clusterDim.y = attribute.val.clusterDim.z = 1;
-    config.attrs = &attribute;
-    config.numAttrs = cut.cluster > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, a);
-    return e == cudaSuccess ? launched() : (cudaGetLastError(), NVFP4_ERR_CUDA);
+    cudaLaunchAttribute attributes[2] = {};
+    int count = 0;
+    if (cluster > 1) {
+        attributes[count].id = cudaLaunchAttributeClusterDimension;
+        attributes[count].val.clusterDim.x = cluster;
+        attributes[count].val.clusterDim.y = attributes[count].val.clusterDim.z = 1;
+        ++count;
+    }
+    if (after) {
+        attributes[count].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attributes[count].val.programmaticStreamSerializationAllowed = 1;
+        ++count;
+    }
+    config.attrs = attributes;
+    config.numAttrs = count;
+    if (cudaLaunchKernelEx(&config, kernel, args...) == cudaSuccess) return launched();
+    cudaGetLastError();
+    return NVFP4_ERR_CUDA;
 }
 
 // Lets `kernel` have `bytes` of dynamic shared memory; without asking it may have 48 KiB with the
@@ -842,29 +996,46 @@ bool allow_smem(size_t bytes) {
 }
 
 nvfp4_status clear_amax(uint32_t* amax, int64_t grid, cudaStream_t stream) {
-    return amax && grid > 1 && cudaMemsetAsync(amax, 0, 4, stream) != cudaSuccess ? NVFP4_ERR_CUDA : NVFP4_OK;
+    if (amax == nullptr || grid == 1) return NVFP4_OK;
+    clear_kernel<<<1, 32, 0, stream>>>(amax);
+    return launched();
 }
 
 template <typename T, int N, int LANES, bool SHIFTED>
-nvfp4_status launch_norm(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
-    constexpr auto kernel = norm_kernel<T, N, LANES, SHIFTED>;
+nvfp4_status launch_group(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
+    constexpr auto kernel = norm_group_kernel<T, N, LANES, SHIFTED>;
     const size_t smem = size_t(kForwardStages) * N * sizeof(T) * cut.threads;
     if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
     const int64_t parts = parts_of(cut, a.rows, int64_t(sm_count()) * resident(forward_registers(N), cut.threads), sizeof(T));
     if (clear_amax(a.amax, parts * cut.cluster, stream) != NVFP4_OK) return NVFP4_ERR_CUDA;
-    return launch_rows<NormArgs>(kernel, a, parts, cut, smem, stream);
+    return launch<NormArgs>(kernel, dim3(static_cast<unsigned>(parts * cut.cluster)), cut.threads, cut.cluster, smem,
+                                  a.amax && parts * cut.cluster > 1, stream, a);
+}
+
+template <typename T, int N, int WARPS, bool SHIFTED>
+nvfp4_status launch_norm(const NormArgs& a, cudaStream_t stream) {
+    constexpr auto kernel = norm_kernel<T, N, WARPS, SHIFTED>;
+    constexpr size_t smem = kWideThreads * N * sizeof(T) * (sizeof(T) == 2 ? 2 : 1) + size_t(WARPS) * 32 * N * 8;
+    if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
+    constexpr int64_t unit = 16 / sizeof(T);
+    const int64_t sms = sm_count(), room = !SHIFTED || sms % unit == 0 ? sms : std::max(unit, sms / unit * unit);
+    const int64_t grid = std::min(a.rows, room);
+    if (clear_amax(a.amax, grid, stream) != NVFP4_OK) return NVFP4_ERR_CUDA;
+    return launch<NormArgs>(kernel, dim3(static_cast<unsigned>(grid)), kWideThreads, 1, smem, a.amax && grid > 1, stream, a);
 }
 
 template <typename T, bool SHIFTED>
 nvfp4_status dispatch_norm(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
-    switch (cut.lanes) {
-        case 8: return launch_norm<T, 8, 8, SHIFTED>(a, cut, stream);
-        case 16: return launch_norm<T, 8, 16, SHIFTED>(a, cut, stream);
-        case 32:
-            return cut.elements == 8 ? launch_norm<T, 8, 32, SHIFTED>(a, cut, stream) : launch_norm<T, 16, 32, SHIFTED>(a, cut, stream);
-        case kCta: return launch_norm<T, 16, kCta, SHIFTED>(a, cut, stream);
-        default: return launch_norm<T, 16, kCluster, SHIFTED>(a, cut, stream);
-    }
+    if (cut.lanes == 8) return launch_group<T, 8, 8, SHIFTED>(a, cut, stream);
+    if (cut.lanes == 16) return launch_group<T, 8, 16, SHIFTED>(a, cut, stream);
+    if (cut.lanes == 32 && cut.elements == 8) return launch_group<T, 8, 32, SHIFTED>(a, cut, stream);
+    const int need = a.cols + (SHIFTED ? kUnit<T> - 1 : 0);
+    if (need <= 512) return launch_norm<T, 16, 1, SHIFTED>(a, stream);
+    if (need <= 1024) return launch_norm<T, 32, 1, SHIFTED>(a, stream);
+    if (need <= 2048) return launch_norm<T, 64, 1, SHIFTED>(a, stream);
+    if (need <= 4096) return launch_norm<T, 64, 2, SHIFTED>(a, stream);
+    if (need <= 8192) return launch_norm<T, 64, 4, SHIFTED>(a, stream);
+    return launch_group<T, 16, kCluster, SHIFTED>(a, cut, stream);
 }
 
 unsigned long_threads(int64_t cols) { return static_cast<unsigned>(std::min<int64_t>(1024, (cols + 31) / 32 * 32)); }
@@ -874,8 +1045,7 @@ nvfp4_status run_norm(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
     if (cut.elements == 0) {
         const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.rows, sm_count() * 2));
         if (clear_amax(a.amax, grid, stream) != NVFP4_OK) return NVFP4_ERR_CUDA;
-        norm_long_kernel<T><<<grid, long_threads(a.cols), 0, stream>>>(a);
-        return launched();
+        return launch<NormArgs>(norm_long_kernel<T>, dim3(grid), long_threads(a.cols), 1, 0, a.amax && grid > 1, stream, a);
     }
     return cut.shifted ? dispatch_norm<T, true>(a, cut, stream) : dispatch_norm<T, false>(a, cut, stream);
 }
@@ -885,7 +1055,8 @@ nvfp4_status launch_grad(const NormGradArgs& a, const Cut& cut, cudaStream_t str
     constexpr auto kernel = norm_grad_kernel<T, N, LANES, SHIFTED>;
     const size_t smem = size_t(kBackwardStages) * 2 * N * sizeof(T) * cut.threads;
     if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
-    return launch_rows<NormGradArgs>(kernel, a, a.parts, cut, smem, stream);
+    return launch<NormGradArgs>(kernel, dim3(static_cast<unsigned>(a.parts * cut.cluster)), cut.threads, cut.cluster, smem,
+                                      false, stream, a);
 }
 
 template <typename T, bool SHIFTED>
@@ -979,12 +1150,10 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, const void* x,
     const nvfp4_status st = x_type == NVFP4_TYPE_F32 ? run_grad<float>(a, cut, stream) : run_grad<bf16>(a, cut, stream);
     if (st != NVFP4_OK || !sums) return st;
     const dim3 grid(static_cast<unsigned>((cols + 31) / 32), 2);
-    if (w_type == NVFP4_TYPE_F32) {
-        norm_join_kernel<float><<<grid, 256, 0, stream>>>(a.sums, a.parts, a.cols, static_cast<float*>(dweight),
-                                                         static_cast<float*>(dbias));
-    } else {
-        norm_join_kernel<bf16><<<grid, 256, 0, stream>>>(a.sums, a.parts, a.cols, static_cast<bf16*>(dweight),
-                                                        static_cast<bf16*>(dbias));
-    }
-    return launched();
+    const float* partial = a.sums;
+    if (w_type == NVFP4_TYPE_F32)
+        return launch<const float*, int, int, float*, float*>(norm_join_kernel<float>, grid, kJoinWarps * 32, 1, 0, true, stream, partial,
+                                                              a.parts, a.cols, static_cast<float*>(dweight), static_cast<float*>(dbias));
+    return launch<const float*, int, int, bf16*, bf16*>(norm_join_kernel<bf16>, grid, kJoinWarps * 32, 1, 0, true, stream, partial, a.parts,
+                                                        a.cols, static_cast<bf16*>(dweight), static_cast<bf16*>(dbias));
 }
