@@ -5,8 +5,8 @@
 // dx = rstd (h - S h / C - xh S(h xh) / C), dw = S_rows dy xh, db = S_rows dy.
 // Both are bound by memory: 4 bytes an element forward and 6 backward in BF16.
 //
-// A row belongs to a group of threads: 8, 16 or 32 lanes of a warp (no barrier), a CTA, or, over
-// 8192 columns, a cluster of CTAs that exchange their sums through shared memory. A thread holds its share of the row in registers from the loads to the result, so x (and dy) are
+// A row belongs to a group of threads: 8, 16 or 32 lanes of a warp (no barrier), some warps of a CTA,
+// or a cluster of CTAs that exchange their sums through shared memory. A thread holds its share of the row in registers from the loads to the result, so x (and dy) are
 // read once, and holds its columns' weight and bias (and their gradients' sums) over all the rows
 // that its group works through. The variance is summed from the held row after the mean is
 // known: no cancellation, at the price of a second reduction.
@@ -117,6 +117,8 @@ struct Columns {
 
     __device__ __forceinline__ Columns(int t, int lanes, int shift, int cols_) : base(t * E - shift), stride(lanes * E), cols(cols_) {}
     __device__ __forceinline__ int start(int q) const { return base + q * stride; }
+    // Whether all columns of a unit exist (for cols >= E).
+    __device__ __forceinline__ bool whole(int q) const { return static_cast<unsigned>(start(q)) <= static_cast<unsigned>(cols - E); }
     __device__ __forceinline__ uint32_t mask(int q) const {
         const int c = start(q);
         if (!SHIFTED) return c < cols ? kAll : 0u;
@@ -465,18 +467,25 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
     if (a.amax) publish_amax(top_bits(top, T{}), a.amax);
 }
 
-// Rows of 257 to 8192 columns. With few elements a thread, the two reductions, the barriers and
+// Rows of 257 to 10240 columns. With few elements a thread, the two reductions, the barriers and
 // the loop cost more instructions than the elements do and bound the kernel (measured at 8192 x
 // 4096 in BF16: 16.6 instructions an element and 29 us with 16 elements a thread). Here a row
-// belongs to WARPS warps with N elements a lane, one CTA of 16 warps has an SM to itself, and
+// belongs to WARPS warps with N elements a lane, one CTA of 16 warps has an SM to itself (as many row groups as fit),  and
 // weight and bias stay in its shared memory as binary32, so that registers hold nothing but the
 // row. The row groups of a CTA take every gridDim.x-th row, which gives all of them one shift.
-constexpr int kWideThreads = 512;
+template <int WARPS>
+constexpr int kWideThreads = 16 / WARPS * WARPS * 32;   // whole row groups
+template <typename T, int Q>
+constexpr int kWideStages = Q <= 2 ? 4 : sizeof(T) == 2 || Q <= 8 ? 2 : 1;   // rows in the ring
+template <typename T, int Q>
+constexpr int kWideCtas = Q * 16 <= 32 ? 2 : 1;                           // CTAs of an SM
 
-template <typename T, int N, int WARPS, bool SHIFTED>
-__global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_constant__ NormArgs a) {
-    constexpr int E = kUnit<T>, Q = N / E, H = E / 2, P = E / 4, S = sizeof(T) == 2 ? 2 : 1;
-    constexpr int kUnits = WARPS * 32 * Q, kGroups = kWideThreads / 32 / WARPS;
+// Q units a lane, of which the units from K on and, in a shifted row, unit 0 may hold columns that
+// do not exist.
+template <typename T, int Q, int K, int WARPS, bool SHIFTED>
+__global__ void __launch_bounds__(kWideThreads<WARPS>, kWideCtas<T, Q>) norm_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int E = kUnit<T>, H = E / 2, P = E / 4, S = kWideStages<T, Q>;
+    constexpr int kUnits = WARPS * 32 * Q, kGroups = 16 / WARPS;
     constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll, kSlot = 512, kStage = Q * kSlot;
     extern __shared__ uint4 ring[];   // rows [warp][S][Q][lane], then weight [P][kUnits], bias [P][kUnits]
     __shared__ float sums[2][kGroups][WARPS];
@@ -486,6 +495,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_cons
     const uintptr_t place = reinterpret_cast<uintptr_t>(a.x) + blockIdx.x * (a.cols * uintptr_t(sizeof(T)));
     const int shift = SHIFTED ? static_cast<int>((place & 15) / sizeof(T)) : 0;
     const Columns<T, Q, SHIFTED> at(t, WARPS * 32, shift, a.cols);
+    const auto may_lack = [](int q) { return q >= K || (SHIFTED && q == 0); };
+    const bool lacks = !at.whole(0) || !at.whole(Q - 1);   // whether any of the lane's columns does not exist
     const int64_t first = blockIdx.x + int64_t(group) * gridDim.x, step = int64_t(gridDim.x) * kGroups;
     const int rows = first < a.rows ? static_cast<int>((a.rows - first + step - 1) / step) : 0;
     const int64_t row_bytes = step * a.cols * int64_t(sizeof(T));
@@ -497,7 +508,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_cons
     const auto fetch = [&](uint32_t slot) {
         if (ahead < rows) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) x.fetch(q, kUnitBytes, slot + q * kSlot, at.mask(q));
+            for (int q = 0; q < Q; ++q) {
+                    x.fetch(q, kUnitBytes, slot + q * kSlot, at.whole(q) ? kAll : at.mask(q));
+            }
         }
         ++ahead;
         x.next += row_bytes;
@@ -505,7 +518,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_cons
     };
 #pragma unroll
     for (int s = 0; s < S; ++s) fetch(slots + s * kStage);
-    for (int u = threadIdx.x; u < kUnits; u += kWideThreads) {
+    for (int u = threadIdx.x; u < kUnits; u += kWideThreads<WARPS>) {
         const Columns<T, 1, SHIFTED> one(u, 0, shift, a.cols);
         float2 w[H], b[H];
         load_param<E>(a.weight, a.w_f32, a.w_vector, one.start(0), one.mask(0), 1.0f, w);
@@ -520,6 +533,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_cons
     const float inv = 1.0f / static_cast<float>(a.cols), eps = a.eps;
     char* y = static_cast<char*>(a.y) + (first * a.cols + at.start(0)) * int64_t(sizeof(T));
     const bool stats = t == 0 && (a.mean || a.rstd), tops = a.amax;
+    // Zero in the place of a unit's columns that do not exist.
+    const auto drop = [&](int q, float2 (&u)[H]) {
+        if (!may_lack(q)) return;
+        if (SHIFTED) {
+            if (lacks) keep(u, at.mask(q));
+        } else {
+            const bool exists = at.start(q) < a.cols;
+#pragma unroll
+            for (int k = 0; k < H; ++k) u[k] = exists ? u[k] : make_float2(0.0f, 0.0f);
+        }
+    };
     // Sum over the row's warps; the two sets alternate as those of WarpSums do.
     const auto row_sum = [&](float v, int which) {
         v = warp_sum(v);
@@ -541,7 +565,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_cons
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             unpack(read_shared(slot + q * kSlot), v[q], T{});
-            if (at.mask(q) != kAll) keep(v[q], at.mask(q));
+            drop(q, v[q]);
 #pragma unroll
             for (int k = 0; k < H; ++k) part[k % 4] = add2(part[k % 4], v[q][k]);
         }
@@ -554,7 +578,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_cons
         for (int q = 0; q < Q; ++q) {
 #pragma unroll
             for (int k = 0; k < H; ++k) v[q][k] = add2(v[q][k], make_float2(-mean, -mean));
-            if (at.mask(q) != kAll) keep(v[q], at.mask(q));
+            drop(q, v[q]);
 #pragma unroll
             for (int k = 0; k < H; ++k) square[k % 4] = fma2(v[q][k], v[q][k], square[k % 4]);
         }
@@ -570,7 +594,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) norm_kernel(const __grid_cons
             }
             const uint4 out = pack(v[q], T{});
             if (tops) join_top(top, out, T{});   // columns that do not exist hold zero
-            store_unit<T>(y + q * kUnitBytes, out, at.mask(q));
+            store_unit<T>(y + q * kUnitBytes, out, may_lack(q) && lacks ? at.mask(q) : kAll);
         }
         if (stats) {
             const int64_t r = first + turn * step;
@@ -1012,16 +1036,38 @@ nvfp4_status launch_group(const NormArgs& a, const Cut& cut, cudaStream_t stream
                                   a.amax && parts * cut.cluster > 1, stream, a);
 }
 
-template <typename T, int N, int WARPS, bool SHIFTED>
+template <typename T, int Q, int K, int WARPS, bool SHIFTED>
 nvfp4_status launch_norm(const NormArgs& a, cudaStream_t stream) {
-    constexpr auto kernel = norm_kernel<T, N, WARPS, SHIFTED>;
-    constexpr size_t smem = kWideThreads * N * sizeof(T) * (sizeof(T) == 2 ? 2 : 1) + size_t(WARPS) * 32 * N * 8;
+    constexpr auto kernel = norm_kernel<T, Q, K, WARPS, SHIFTED>;
+    constexpr size_t smem = size_t(16) * Q * 512 * kWideStages<T, Q> + size_t(WARPS) * 32 * Q * kUnit<T> * 8;
     if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
     constexpr int64_t unit = 16 / sizeof(T);
-    const int64_t sms = sm_count(), room = !SHIFTED || sms % unit == 0 ? sms : std::max(unit, sms / unit * unit);
+    const int64_t ctas = sm_count() * kWideCtas<T, Q>, room = !SHIFTED || ctas % unit == 0 ? ctas : std::max(unit, ctas / unit * unit);
     const int64_t grid = std::min(a.rows, room);
     if (clear_amax(a.amax, grid, stream) != NVFP4_OK) return NVFP4_ERR_CUDA;
-    return launch<NormArgs>(kernel, dim3(static_cast<unsigned>(grid)), kWideThreads, 1, smem, a.amax && grid > 1, stream, a);
+    return launch<NormArgs>(kernel, dim3(static_cast<unsigned>(grid)), kWideThreads<WARPS>, 1, smem, a.amax && grid > 1, stream, a);
+}
+
+// Rows of WARPS warps whose lanes need FROM to 8 (BF16) units; FP32 rows need twice as many, in
+// coarser steps. A row whose shift happens to be 0 may end one unit earlier than the longest shift
+// would have it.
+template <typename T, int WARPS, int FROM, bool SHIFTED>
+nvfp4_status launch_wide(const NormArgs& a, int need, cudaStream_t stream) {
+    constexpr int S = SHIFTED;
+    const int units = (need + WARPS * 256 - 1) / (WARPS * 256);
+    if constexpr (sizeof(T) == 4) {
+        if (FROM <= 2 && units <= 2) return launch_norm<T, 4, 2 - S, WARPS, SHIFTED>(a, stream);
+        if (FROM <= 4 && units <= 4) return launch_norm<T, 8, 4 - S, WARPS, SHIFTED>(a, stream);
+        return launch_norm<T, 16, 8 - S, WARPS, SHIFTED>(a, stream);
+    } else {
+        if constexpr (FROM <= 2) if (units == 2) return launch_norm<T, 2, 1 - S, WARPS, SHIFTED>(a, stream);
+        if constexpr (FROM <= 3) if (units == 3) return launch_norm<T, 3, 2 - S, WARPS, SHIFTED>(a, stream);
+        if constexpr (FROM <= 4) if (units == 4) return launch_norm<T, 4, 3 - S, WARPS, SHIFTED>(a, stream);
+        if constexpr (FROM <= 5) if (units == 5) return launch_norm<T, 5, 4 - S, WARPS, SHIFTED>(a, stream);
+        if constexpr (FROM <= 6) if (units == 6) return launch_norm<T, 6, 5 - S, WARPS, SHIFTED>(a, stream);
+        if constexpr (FROM <= 7) if (units == 7) return launch_norm<T, 7, 6 - S, WARPS, SHIFTED>(a, stream);
+        return launch_norm<T, 8, 7 - S, WARPS, SHIFTED>(a, stream);
+    }
 }
 
 template <typename T, bool SHIFTED>
@@ -1030,11 +1076,11 @@ nvfp4_status dispatch_norm(const NormArgs& a, const Cut& cut, cudaStream_t strea
     if (cut.lanes == 16) return launch_group<T, 8, 16, SHIFTED>(a, cut, stream);
     if (cut.lanes == 32 && cut.elements == 8) return launch_group<T, 8, 32, SHIFTED>(a, cut, stream);
     const int need = a.cols + (SHIFTED ? kUnit<T> - 1 : 0);
-    if (need <= 512) return launch_norm<T, 16, 1, SHIFTED>(a, stream);
-    if (need <= 1024) return launch_norm<T, 32, 1, SHIFTED>(a, stream);
-    if (need <= 2048) return launch_norm<T, 64, 1, SHIFTED>(a, stream);
-    if (need <= 4096) return launch_norm<T, 64, 2, SHIFTED>(a, stream);
-    if (need <= 8192) return launch_norm<T, 64, 4, SHIFTED>(a, stream);
+    if (need <= 2048) return launch_wide<T, 1, 2, SHIFTED>(a, need, stream);
+    if (need <= 4096) return launch_wide<T, 2, 5, SHIFTED>(a, need, stream);
+    if (need <= 6144) return launch_wide<T, 3, 6, SHIFTED>(a, need, stream);
+    if (need <= 8192) return launch_wide<T, 4, 7, SHIFTED>(a, need, stream);
+    if (need <= 10240) return launch_wide<T, 5, 7, SHIFTED>(a, need, stream);
     return launch_group<T, 16, kCluster, SHIFTED>(a, cut, stream);
 }
 

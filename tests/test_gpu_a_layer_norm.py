@@ -80,6 +80,15 @@ def test_forward(gpu, rows, cols, xt, wt):
     check_forward(nv.layer_norm_forward(x, w, b, 1e-5, with_amax=True), x, w, b, 1e-5, xt)
 
 
+@pytest.mark.parametrize("edge", [256, 512, 768, 1024, 1280, 1536, 1792, 2048, 2560, 3584, 4096, 4608, 5376, 6144, 7168, 8192, 8960, 10240])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_forward_at_the_edges_of_the_row_cuts(gpu, edge, xt):
+    """Widths around every number of units a lane: each shift, each last unit whole, partial or missing."""
+    for cols in (*range(edge - 8, edge + 9), edge + 31):
+        x, w, b, _ = make(9, cols, xt, "f32", seed=cols)
+        check_forward(nv.layer_norm_forward(x, w, b, 1e-5, with_amax=True), x, w, b, 1e-5, xt)
+
+
 @pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("cols", [48, 333, 4096])
 def test_forward_without_weight_or_bias(gpu, cols, weight, bias):
