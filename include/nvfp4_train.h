@@ -139,12 +139,14 @@ typedef struct {
     uint32_t reserved[2];
 } nvfp4_adamw_control;
 
-/* One AdamW step over a list, in place. With t the steps taken before this one plus one,
- * g = scale * grad, in binary32 with every operation rounded (no contraction):
- *   m' = beta1 * m + (1 - beta1) * g
- *   v' = beta2 * v + (1 - beta2) * (g * g);   u' = sqrt(v')
- *   p' = p * (1 - lr * weight_decay) - (m' / (u' / sqrt(1 - beta2^t) + eps)) * (lr / (1 - beta1^t))
- * where (1 - beta2^t)^-1/2 and lr / (1 - beta1^t) are taken in binary64 and rounded once.
+/* One AdamW step over a list, in place. With t the steps taken before this one plus one and
+ * g = scale * grad, in binary32, fma(a, b, c) = a * b + c rounded once:
+ *   m' = fma(m, beta1, (1 - beta1) * g)
+ *   v' = fma(v, beta2, (1 - beta2) * (g * g));   u' = sqrt(v')
+ *   p' = fma(m' / fma(u', r, eps), -lr / (1 - beta1^t), p * (1 - lr * weight_decay)),  r = (1 - beta2^t)^-1/2
+ * where r and lr / (1 - beta1^t) are taken in binary64 and rounded once. Beside 8-bit states the
+ * root is the hardware's approximation (2^-23) and the quotient the product with its approximate
+ * reciprocal (2^-23).
  * Parameters. FP32: p. BF16 with a master: p is the master, param = BF16(p'), to nearest even.
  * BF16 without one: p' is rounded stochastically, because an update is mostly far below half a
  * BF16 step, and rounding to nearest would lose it every time.

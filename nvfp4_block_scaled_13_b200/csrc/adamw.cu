@@ -5,8 +5,8 @@
 // costs, with BF16 gradients, 28 bytes (BF16 parameter with FP32 master, 32-bit states) or
 // 10.125 (BF16 parameter, 8-bit states) and some 40 operations, so memory bounds the step.
 //
-// The step's arithmetic is plain binary32 with every operation rounded on its own, so it has
-// one right answer, bit for bit. 8-bit states are E4M3 codes in blocks of 32 with an E8M0 byte:
+// The step's arithmetic is binary32 with its fused operations stated one by one, so with 32-bit
+// states it has one right answer, bit for bit. 8-bit states are E4M3 codes in blocks of 32 with an E8M0 byte:
 // the scale is a power of two, so decoding and scaling are exact and cost one multiplication.
 #include <float.h>
 #include <math.h>
@@ -90,15 +90,15 @@ __device__ __forceinline__ void put8(T* p, int64_t i, int64_t n, bool whole, con
 
 __device__ __forceinline__ float power_of_two(uint32_t biased) { return __uint_as_float(biased << 23); }
 
-__device__ __forceinline__ void decode4(uint32_t codes, float scale, float* out) {
+// Four codes as two pairs, without their scale.
+__device__ __forceinline__ void decode4(uint32_t codes, float2* out) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         uint32_t h2;
-        asm("{\n\t.reg .b16 lo;\n\tmov.b32 {lo, _}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h2) : "r"(codes >> (16 * k)));
-        float lo, hi;
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h2));
-        out[2 * k] = lo * scale;
-        out[2 * k + 1] = hi * scale;
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h2) : "r"(codes >> (16 * k)));
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(out[k].x), "=f"(out[k].y)
+            : "r"(h2));
     }
 }
 
@@ -106,36 +106,57 @@ __device__ __forceinline__ void decode4(uint32_t codes, float scale, float* out)
 // maximum above 448 * 2^(s - 127) to the next power.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top) { return max((top + 0x1FFFFFu) >> 23, 9u) - 8u; }
 
-__device__ __forceinline__ uint32_t block_top(const float (&v)[8]) {
-    uint32_t top = magnitude(v[0]);
+// The largest magnitude of a block, of which four threads hold eight elements each.
+__device__ __forceinline__ uint32_t block_top(const float2 (&v)[4]) {
+    uint32_t top = 0;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) top = max(top, magnitude(v[j]));
-    top = max(top, __shfl_xor_sync(kFull, top, 1));   // four threads hold a block
+    for (int k = 0; k < 4; ++k) top = max(top, max(magnitude(v[k].x), magnitude(v[k].y)));
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
     return max(top, __shfl_xor_sync(kFull, top, 2));
 }
 
-__device__ __forceinline__ uint2 encode_nearest(const float (&v)[8], float inverse) {
+__device__ __forceinline__ uint2 encode_nearest(const float2 (&v)[4], float inverse) {
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * k + 1] * inverse), "f"(v[4 * k] * inverse));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * k + 3] * inverse), "f"(v[4 * k + 2] * inverse));
-        w[k] = uint32_t(lo) | (uint32_t(hi) << 16);
+        const float2 a = mul2(v[2 * k], make_float2(inverse, inverse)), b = mul2(v[2 * k + 1], make_float2(inverse, inverse));
+        asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+            "mov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(w[k])
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     }
     return make_uint2(w[0], w[1]);
 }
 
-// u >= 0. Scaled by 2^-120, a value's exponent field is E4M3's (subnormals included), so its top
-// bits from bit 20 on are the code, and random bits added below them round it stochastically.
-__device__ __forceinline__ uint2 encode_stochastic(const float (&u)[8], float inverse, uint32_t word) {
-    uint32_t w[2] = {0u, 0u};
+// u >= 0. Scaled by 2^-120, a value's exponent field is E4M3's (subnormals included), so its bits
+// from bit 20 on are the code, and random bits added below them round it stochastically. The sum
+// is taken four bits higher, which leaves the code in the top byte. Codes 0 of positive values,
+// NaN and infinity are rare and left to a second look: 0 shows as a byte without a bit, and a
+// block with NaN or infinity by its largest magnitude.
+__device__ __forceinline__ uint2 encode_stochastic(const float2 (&u)[4], float inverse, uint32_t word, uint32_t top) {
+    uint32_t w[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t low = __float_as_uint(u[j] * inverse * 0x1p-120f);
-        uint32_t code = (low + (((word + j * kGolden) & 0xFFFFu) << 4)) >> 20;
-        code = min(max(code, u[j] > 0.0f ? 1u : 0u), 0x7Fu);   // NaN and infinity: the NaN code
-        w[j >> 2] |= code << (8 * (j & 3));
+    for (int k = 0; k < 2; ++k) {
+        uint32_t sum[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 y = mul2(mul2(u[2 * k + j / 2], make_float2(inverse, inverse)), make_float2(0x1p-120f, 0x1p-120f));
+            const uint32_t random = word + (4 * k + j) * kGolden;
+            sum[j] = (__float_as_uint(j & 1 ? y.y : y.x) << 4) + __byte_perm(random, 0, 0x4104);
+        }
+        w[k] = __byte_perm(__byte_perm(sum[0], sum[1], 0x0073), __byte_perm(sum[2], sum[3], 0x0073), 0x5410);
+    }
+    if (top >= 0x7F800000u || ((w[0] - 0x01010101u) & ~w[0] & 0x80808080u) || ((w[1] - 0x01010101u) & ~w[1] & 0x80808080u)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = j & 1 ? u[j / 2].y : u[j / 2].x;
+            const int at = 8 * (j & 3);
+            if (!(x < INFINITY)) {
+                w[j >> 2] = (w[j >> 2] & ~(0xFFu << at)) | (0x7Fu << at);
+            } else if (x > 0.0f && !(w[j >> 2] >> at & 0xFFu)) {
+                w[j >> 2] |= 1u << at;
+            }
+        }
     }
     return make_uint2(w[0], w[1]);
 }
@@ -190,6 +211,71 @@ struct StepArgs {
     uint32_t* amax;
 };
 
+// Root and quotient. 32-bit states take them as IEEE has them. Beside 8-bit states, whose step
+// is bound by the instructions, the hardware's approximations do (relative errors of at most 2^-23
+// each): u is then rounded to 4 bits, and the update is added to a parameter that it
+// changes in its last bits.
+template <bool EIGHT>
+__device__ __forceinline__ float root_of(float v) {
+    if (!EIGHT) return sqrtf(v);
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+template <bool EIGHT>
+__device__ __forceinline__ float quotient(float a, float b) {
+    if (!EIGHT) return a / b;
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(b));
+    return a * r;
+}
+
+// Rounds to BF16 with the high half of each element's random word added to the dropped bits.
+__device__ __forceinline__ uint4 round_stochastic(const float2 (&p)[4], uint32_t word) {
+    uint32_t w[4];
+    float2 finite = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t a = __float_as_uint(p[k].x) + ((word + 2 * k * kGolden) >> 16);
+        const uint32_t b = __float_as_uint(p[k].y) + ((word + (2 * k + 1) * kGolden) >> 16);
+        w[k] = __byte_perm(a, b, 0x7632);
+        finite = fma2(p[k], make_float2(0.0f, 0.0f), finite);
+    }
+    // NaN and infinity are left to the conversion: adding to their bits could carry into the sign.
+    if (!(finite.x + finite.y == 0.0f)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (!(fabsf(p[k].x) < INFINITY)) w[k] = (w[k] & 0xFFFF0000u) | to_bf16(p[k].x);
+            if (!(fabsf(p[k].y) < INFINITY)) w[k] = (w[k] & 0xFFFFu) | (uint32_t(to_bf16(p[k].y)) << 16);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void fetch_pairs(const T* p, int64_t i, int64_t n, bool whole, float2 (&v)[4]) {
+    float f[8];
+    fetch8(p, i, n, whole, f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = make_float2(f[2 * k], f[2 * k + 1]);
+}
+__device__ __forceinline__ void put_pairs(float* p, int64_t i, int64_t n, bool whole, const float2 (&v)[4]) {
+    const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+    put8(p, i, n, whole, f);
+}
+__device__ __forceinline__ void put_bf16(bf16* p, int64_t i, int64_t n, bool whole, const uint4& w) {
+    if (whole) {
+        *reinterpret_cast<uint4*>(p + i) = w;
+    } else {
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) p[i + j].bits = static_cast<uint16_t>(a[j / 2] >> (16 * (j & 1)));
+    }
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // One chunk; the maximum of the stored parameters is joined to `top`.
 template <uint32_t KIND>
 __device__ __forceinline__ void step_chunk(const Tensor& t, int64_t lo, int64_t hi, const Factors& f, uint32_t& top) {
@@ -199,74 +285,91 @@ __device__ __forceinline__ void step_chunk(const Tensor& t, int64_t lo, int64_t 
     for (int64_t base = lo; base < hi; base += kTile) {
         const int64_t i = base + threadIdx.x * 8;
         const bool whole = (t.variant & kVector) && i + 8 <= n;
-        float g[8], p[8], m[8], u[8];
+        float2 g[4], p[4], m[4], u[4];
         if (GRAD_F32) {
-            fetch8(static_cast<const float*>(t.d.grad), i, n, whole, g);
+            fetch_pairs(static_cast<const float*>(t.d.grad), i, n, whole, g);
         } else {
-            fetch8(static_cast<const bf16*>(t.d.grad), i, n, whole, g);
+            fetch_pairs(static_cast<const bf16*>(t.d.grad), i, n, whole, g);
         }
         if (MASTER) {
-            fetch8(static_cast<const float*>(t.d.master), i, n, whole, p);
+            fetch_pairs(t.d.master, i, n, whole, p);
         } else if (PARAM_F32) {
-            fetch8(static_cast<const float*>(t.d.param), i, n, whole, p);
+            fetch_pairs(static_cast<const float*>(t.d.param), i, n, whole, p);
         } else {
-            fetch8(static_cast<const bf16*>(t.d.param), i, n, whole, p);
+            fetch_pairs(static_cast<const bf16*>(t.d.param), i, n, whole, p);
         }
+        float sm = 0.0f, su = 0.0f;
         if (EIGHT) {
             uint2 cm, cu;
             fetch_codes(static_cast<const uint8_t*>(t.d.exp_avg), i, n, whole, cm);
             fetch_codes(static_cast<const uint8_t*>(t.d.exp_avg_sq), i, n, whole, cu);
-            const float sm = i < n ? power_of_two(t.d.exp_avg_scale[i >> 5]) : 0.0f;
-            const float su = i < n ? power_of_two(t.d.exp_avg_sq_scale[i >> 5]) : 0.0f;
-            decode4(cm.x, sm, m);
-            decode4(cm.y, sm, m + 4);
-            decode4(cu.x, su, u);
-            decode4(cu.y, su, u + 4);
+            if (i < n) {
+                sm = power_of_two(t.d.exp_avg_scale[i >> 5]);
+                su = power_of_two(t.d.exp_avg_sq_scale[i >> 5]);
+            }
+            decode4(cm.x, m);
+            decode4(cm.y, m + 2);
+            decode4(cu.x, u);
+            decode4(cu.y, u + 2);
         } else {
-            fetch8(static_cast<const float*>(t.d.exp_avg), i, n, whole, m);
-            fetch8(static_cast<const float*>(t.d.exp_avg_sq), i, n, whole, u);
+            fetch_pairs(static_cast<const float*>(t.d.exp_avg), i, n, whole, m);
+            fetch_pairs(static_cast<const float*>(t.d.exp_avg_sq), i, n, whole, u);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            g[j] *= f.scale;
-            m[j] = m[j] * f.beta1 + g[j] * f.rest1;
-            const float v = (EIGHT ? u[j] * u[j] : u[j]) * f.beta2 + (g[j] * g[j]) * f.rest2;
-            const float root = sqrtf(v);
-            u[j] = EIGHT ? root : v;
-            p[j] = p[j] * keep - (m[j] / (root * f.root + f.eps)) * f.rate;
+        for (int k = 0; k < 4; ++k) {
+            g[k] = mul2(g[k], both(f.scale));
+            if (EIGHT) {
+                m[k] = mul2(m[k], both(sm));
+                u[k] = mul2(u[k], both(su));
+                u[k] = mul2(u[k], u[k]);
+            }
+            m[k] = fma2(m[k], both(f.beta1), mul2(g[k], both(f.rest1)));
+            u[k] = fma2(u[k], both(f.beta2), mul2(mul2(g[k], g[k]), both(f.rest2)));
+            const float2 root = make_float2(root_of<EIGHT>(u[k].x), root_of<EIGHT>(u[k].y));
+            const float2 under = fma2(root, both(f.root), both(f.eps));
+            const float2 ratio = make_float2(quotient<EIGHT>(m[k].x, under.x), quotient<EIGHT>(m[k].y, under.y));
+            p[k] = fma2(ratio, both(-f.rate), mul2(p[k], both(keep)));
+            if (EIGHT) u[k] = root;
         }
         const uint32_t word = mix(static_cast<uint32_t>((t.d.first + i) >> 3) ^ f.key);
-        if (MASTER) put8(t.d.master, i, n, whole, p);
         if (PARAM_F32) {
-            put8(static_cast<float*>(t.d.param), i, n, whole, p);
+            put_pairs(static_cast<float*>(t.d.param), i, n, whole, p);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i + 2 * k < n) top = max(top, magnitude(p[k].x));
+                if (i + 2 * k + 1 < n) top = max(top, magnitude(p[k].y));
+            }
         } else {
-            if (!MASTER) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    // NaN is left to the conversion: adding to its bits could carry into the sign
-                    const uint32_t bits = __float_as_uint(p[j]), sum = bits + ((word + j * kGolden) >> 16);
-                    p[j] = p[j] == p[j] ? __uint_as_float(sum & 0xFFFF0000u) : p[j];
-                }
-            }
-            put8(static_cast<bf16*>(t.d.param), i, n, whole, p);
+            uint4 w;
             if (MASTER) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = __uint_as_float(uint32_t(to_bf16(p[j])) << 16);
+                put_pairs(t.d.master, i, n, whole, p);
+                w = make_uint4(to_bf16x2(p[0].x, p[0].y), to_bf16x2(p[1].x, p[1].y), to_bf16x2(p[2].x, p[2].y), to_bf16x2(p[3].x, p[3].y));
+            } else {
+                w = round_stochastic(p, word);
             }
-        }
+            put_bf16(static_cast<bf16*>(t.d.param), i, n, whole, w);
+            uint32_t best = 0;   // of two halves
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, i + j < n ? magnitude(p[j]) : 0u);
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v = a[k];
+                if (i + 2 * k + 1 >= n) v = i + 2 * k >= n ? 0u : v & 0xFFFFu;
+                asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %1;\n\tmax.NaN.bf16x2 %0, %0, m;\n\t}" : "+r"(best) : "r"(v));
+            }
+            top = max(top, max(best << 16, best & 0xFFFF0000u));
+        }
         if (EIGHT) {
-            const uint32_t bm = scale_byte(block_top(m)), bu = scale_byte(block_top(u));
+            const uint32_t tm = block_top(m), tu = block_top(u);
+            const uint32_t bm = scale_byte(tm), bu = scale_byte(tu);
             put_codes(static_cast<uint8_t*>(t.d.exp_avg), i, n, whole, encode_nearest(m, power_of_two(254u - bm)));
-            put_codes(static_cast<uint8_t*>(t.d.exp_avg_sq), i, n, whole, encode_stochastic(u, power_of_two(254u - bu), word));
+            put_codes(static_cast<uint8_t*>(t.d.exp_avg_sq), i, n, whole, encode_stochastic(u, power_of_two(254u - bu), word, tu));
             if ((threadIdx.x & 3) == 0 && i < n) {
                 t.d.exp_avg_scale[i >> 5] = static_cast<uint8_t>(bm);
                 t.d.exp_avg_sq_scale[i >> 5] = static_cast<uint8_t>(bu);
             }
         } else {
-            put8(static_cast<float*>(t.d.exp_avg), i, n, whole, m);
-            put8(static_cast<float*>(t.d.exp_avg_sq), i, n, whole, u);
+            put_pairs(static_cast<float*>(t.d.exp_avg), i, n, whole, m);
+            put_pairs(static_cast<float*>(t.d.exp_avg_sq), i, n, whole, u);
         }
     }
 }

@@ -341,10 +341,10 @@ struct Group {
     __device__ __forceinline__ Group(const void* x, int64_t all_rows, int cols) {
         constexpr unsigned L = LANES > 0 ? LANES : 1;
         int64_t base = blockIdx.x, ctas = gridDim.x;
-        lanes = LANES > 0 ? LANES : blockDim.x;
-        t = LANES > 0 ? threadIdx.x % L : threadIdx.x;
-        groups = LANES > 0 ? blockDim.x / L : 1;
-        index = LANES > 0 ? threadIdx.x / L : 0;
+        lanes = LANES > 0 ? LANES : static_cast<int>(blockDim.x);
+        t = static_cast<int>(LANES > 0 ? threadIdx.x % L : threadIdx.x);
+        groups = LANES > 0 ? static_cast<int>(blockDim.x / L) : 1;
+        index = LANES > 0 ? static_cast<int>(threadIdx.x / L) : 0;
         if (LANES == kCluster) {
             const int size = static_cast<int>(cluster_size());
             t += static_cast<int>(cluster_rank() * blockDim.x);

@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "ptx.cuh"
+
 namespace nvfp4_train {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -83,10 +85,10 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Two binary32 lanes in one instruction, each rounded as its scalar form.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+// Two binary32 lanes in one instruction, each rounded as its scalar form (never contracted).
+using nvfp4::add2;
+using nvfp4::fma2;
+using nvfp4::mul2;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

@@ -1,10 +1,11 @@
 """AdamW over lists of tensors and the gradient norm, on the GPU.
 
-The step's arithmetic is binary32 with every operation rounded, so parameters, states, codes and
-scale bytes are compared bit for bit with the same operations in numpy; and with the definition in
-binary64, where u = 2^-24: m within 4 u (|b1 m| + |r1 g|) (three roundings and the rounded
+The step's arithmetic is binary32 with every operation rounded, so parameters and states are compared
+bit for bit with the same operations in numpy (beside 8-bit states up to two approximations of 2^-23,
+as assert_step says); and with the definition in binary64, where u = 2^-24: m within 4 u (|b1 m| + |r1 g|) (three roundings and the rounded
 coefficients), v within 8 u v, p within 3 u |p| + 16 u |update| + (the error of m) rate / denominator
-(products, the quotient, the root, the factors), then half a step of a type that is rounded to
+(products, the quotient, the root, the factors; 24 u beside 8-bit states, whose root and reciprocal are
+off by up to 2 u more and whose quotient has one more rounding), then half a step of a type that is rounded to
 nearest, or a whole one of a stochastic rounding. 8-bit values: half an E4M3 step for m (2^-4 of
 the value, or 2^-10 of the block's power of two), a whole one for u. Underflow takes at most 2^-147 from v, and
 so 2^-73.5 from its root.
@@ -83,8 +84,7 @@ def check(plan, olds, lr, scale, steps, decay=0.1):
         kw = dict(lr=lr, decay=decay * (i % 2), betas=plan.betas, eps=plan.eps, scale=scale, steps=steps)
         want = R.adamw_bits(p, g, m, v, param_bf16=bf16, master=master, bits=plan.state_bits, first=plan.offsets[i], seed=plan.seed, **kw)
         got = {"param": values(plan.params[i]), **{k: raw(t) for k, t in plan.state(i).items()}}
-        for k, w in want.items():
-            np.testing.assert_array_equal(got[k], w, err_msg=f"tensor {i} of {len(p)}: {k}")
+        R.assert_step(got, want, plan.state_bits, f"tensor {i} of {len(p)}")
         if plan.amax is not None:
             assert plan.amax[i].item() == np.abs(got["param"]).max()
         # the definition
@@ -93,7 +93,7 @@ def check(plan, olds, lr, scale, steps, decay=0.1):
             v = root * root
         p1, m1, v1, size_m, update, per_m = R.adamw64(p, g, m, v, **kw)
         tol_m = 4 * U * size_m + 2.0 ** -147          # and what underflow takes from each of three operations
-        tol_p = 3 * U * np.abs(p) + 16 * U * update + tol_m * per_m
+        tol_p = 3 * U * np.abs(p) + (16 if plan.state_bits == 32 else 24) * U * update + tol_m * per_m
         full = got["master"].astype(np.float64) if master else got["param"].astype(np.float64)
         half = 0.0 if master or not bf16 else 2.0 ** -7
         assert (np.abs(full - p1) <= tol_p + half * (np.abs(p1) + tol_p) + 2.0 ** -133).all()
@@ -104,7 +104,7 @@ def check(plan, olds, lr, scale, steps, decay=0.1):
             assert (np.abs(got["exp_avg_sq"] - v1) <= 8 * U * v1 + 2.0 ** -147).all()
         else:
             n = len(p)
-            for name, x, tol, step in (("exp_avg", m1, tol_m, 0.5), ("exp_avg_sq", np.sqrt(v1), 5 * U * np.sqrt(v1) + 2.0 ** -73.5, 1.0)):
+            for name, x, tol, step in (("exp_avg", m1, tol_m, 0.5), ("exp_avg_sq", np.sqrt(v1), 7 * U * np.sqrt(v1) + 2.0 ** -73.5, 1.0)):
                 unit = R.spread(R.power(got[name + "_scale"]), n).astype(np.float64)
                 value = R.decode(got[name], got[name + "_scale"])
                 assert (np.abs(value - x) <= tol + step * np.maximum(2.0 ** -3 * np.abs(x), 2.0 ** -9 * unit) * (1 + 4 * U)).all()

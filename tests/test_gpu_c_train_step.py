@@ -80,7 +80,9 @@ def test_steps_in_a_run(gpu, bits, masters):
         for i, ((old, m, v), g) in enumerate(zip(olds, grads)):
             w = R.adamw_bits(old, g, m, v, param_bf16=True, master=masters, bits=bits, lr=1e-3, decay=(0.0, 0.0, 0.1, 0.1)[i],
                              betas=s.plan.betas, eps=s.plan.eps, scale=scale.item(), steps=step, first=s.plan.offsets[i], seed=0)
-            np.testing.assert_array_equal(s.params[i].detach().float().cpu().numpy().reshape(-1), w["param"])
+            got = {k: (t.view(torch.uint8) if t.element_size() == 1 else t).cpu().numpy() for k, t in s.plan.state(i).items()}
+            got["param"] = s.params[i].detach().float().cpu().numpy().reshape(-1)
+            R.assert_step(got, w, bits)
             # the amax that the step wrote is the one the quantizer would take
             if s.params[i].dim() == 2:
                 assert s.plan.amax[i].item() == nv.amax(s.params[i].detach()).item()

@@ -24,6 +24,11 @@ def from_bf16_bits(b):
     return (b.astype(np.uint32) << 16).view(np.float32)
 
 
+def bf16_stochastic(x, word):
+    b = ((np.asarray(x, np.float32).view(np.uint32).astype(np.uint64) + (word >> np.uint64(16))) >> np.uint64(16)) << np.uint64(16)
+    return b.astype(np.uint32).view(np.float32)
+
+
 def mix(a):
     a = np.asarray(a, np.uint64)
     a = a ^ (a >> np.uint64(16))
@@ -96,8 +101,16 @@ def encode_stochastic(u, word):
     return np.maximum(code, (u > 0).astype(np.uint64)).astype(np.uint8), s
 
 
+def fma(a, b, c):
+    """a * b + c rounded once to binary32 (the product is exact in 64 bits of significand, and the
+    sum's rounding there changes the result for one in 2^40)."""
+    wide = np.longdouble
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        return (np.asarray(a, wide) * np.asarray(b, wide) + np.asarray(c, wide)).astype(np.float32)
+
+
 def adamw_bits(p, g, m, v, *, param_bf16, master, bits, lr, decay, betas, eps, scale, steps, first, seed):
-    """One step in binary32, each operation rounded. p: float32 values of the master or parameter; m, v:
+    """One step in binary32, as the header states it. p: float32 values of the master or parameter; m, v:
     float32 arrays, or (codes, scale bytes) of the first moment and of the second one's root."""
     f = np.float32
     n = len(p)
@@ -110,18 +123,18 @@ def adamw_bits(p, g, m, v, *, param_bf16, master, bits, lr, decay, betas, eps, s
     if bits == 8:
         m, root = decode(*m), decode(*v)
         v = root * root
-    m = m * b1 + g * r1
-    v = v * b2 + (g * g) * r2
+    m = fma(m, b1, g * r1)
+    v = fma(v, b2, (g * g) * r2)
     root = np.sqrt(v)
-    q = p * keep - (m / (root * root_factor + f(eps))) * rate
+    ratio = m / fma(root, root_factor, f(eps))
+    q = fma(ratio, -rate, p * keep)
     assert m.dtype == v.dtype == q.dtype == np.float32
     word = words(n, first, seed, steps)
-    out = {}
+    out = {"_q": q, "_root": root, "_word": word, "_update": np.abs(ratio * rate)}
     if param_bf16 and master:
         out["master"], out["param"] = q, bf16_round(q)
     elif param_bf16:
-        b = ((q.view(np.uint32).astype(np.uint64) + (word >> np.uint64(16))) >> np.uint64(16)) << np.uint64(16)
-        out["param"] = b.astype(np.uint32).view(np.float32)
+        out["param"] = bf16_stochastic(q, word)
     else:
         out["param"] = q
     if bits == 8:
@@ -130,6 +143,41 @@ def adamw_bits(p, g, m, v, *, param_bf16, master, bits, lr, decay, betas, eps, s
     else:
         out["exp_avg"], out["exp_avg_sq"] = m, v
     return out
+
+
+def assert_step(got, want, bits, what=""):
+    """got: what a step left (param, states, master) as arrays; want: adamw_bits'.
+
+    Beside 32-bit states every bit agrees. Beside 8-bit ones the root and the reciprocal under m are
+    approximations of 2^-23 each: m's codes and scales agree, u's are those of a root that much
+    larger or smaller, and the parameter those of an update within 2^-21 of itself (both errors, the
+    rounded product in place of the rounded quotient, and the halves of the rounding) and one more
+    rounding of the sum."""
+    if bits == 32:
+        for k, w in want.items():
+            if k[0] != "_":
+                np.testing.assert_array_equal(got[k], w, err_msg=f"{what}: {k}")
+        return
+    for k in ("exp_avg", "exp_avg_scale"):
+        np.testing.assert_array_equal(got[k], want[k], err_msg=f"{what}: {k}")
+    f = np.float32
+    low, high = (encode_stochastic((want["_root"] * f(1 + e)).astype(f), want["_word"]) for e in (-2.0 ** -22, 2.0 ** -22))
+    scale = got["exp_avg_sq_scale"]
+    assert ((scale == low[1]) | (scale == high[1])).all(), what
+    same = spread(low[1] == high[1], len(low[0]))
+    code = got["exp_avg_sq"]
+    assert ((code >= low[0]) & (code <= high[0]))[same].all(), what
+    assert same.mean() > 0.99 or len(same) < 4000
+    q = want["_q"].astype(np.float64)
+    slack = 2.0 ** -21 * want["_update"] + 2.0 ** -23 * np.abs(q) + 2.0 ** -148
+    if "master" in want:
+        assert (np.abs(got["master"] - q) <= slack).all(), what
+        np.testing.assert_array_equal(got["param"], bf16_round(got["master"]))
+    elif (want["param"] == want["_q"]).all():
+        assert (np.abs(got["param"] - q) <= slack).all(), what
+    else:
+        ends = [bf16_stochastic((q + e * slack).astype(f), want["_word"]) for e in (-1.01, 1.01)]
+        assert ((got["param"] >= ends[0]) & (got["param"] <= ends[1])).all(), what
 
 
 def adamw64(p, g, m, v, *, lr, decay, betas, eps, scale, steps):
