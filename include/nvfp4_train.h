@@ -105,7 +105,7 @@ NVFP4_API int64_t nvfp4_tensor_plan_bytes(const nvfp4_opt_tensor* tensors, int64
  * tensors. Refused: a NULL pointer where one is needed (NVFP4_ERR_NULL); a negative length, a
  * total of 2^34 elements or more, `first` not a multiple of 8 (NVFP4_ERR_SHAPE); a pointer that
  * is not aligned to its element (NVFP4_ERR_ALIGN); an unknown type, state_bits other than 32
- * and 8, a master of a param that is not BF16, a non-finite weight decay, both kinds in one
+ * and 8 or not the same in the whole list, a master of a param that is not BF16, a non-finite weight decay, both kinds in one
  * list, or memory that one tensor writes and another one writes or reads (NVFP4_ERR_VALUE). */
 NVFP4_API nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64_t count, void* image,
                                          int64_t image_bytes, int64_t* chunks);
@@ -143,9 +143,9 @@ typedef struct {
  * g = scale * grad, in binary32, fma(a, b, c) = a * b + c rounded once:
  *   m' = fma(m, beta1, (1 - beta1) * g)
  *   v' = fma(v, beta2, (1 - beta2) * (g * g));   u' = sqrt(v')
- *   p' = fma(m' / fma(u', r, eps), -lr / (1 - beta1^t), p * (1 - lr * weight_decay)),  r = (1 - beta2^t)^-1/2
- * where r and lr / (1 - beta1^t) are taken in binary64 and rounded once. Beside 8-bit states the
- * root is the hardware's approximation (2^-23) and the quotient the product with its approximate
+ *   p' = fma(m' / fma(u', r, eps), -lr / (1 - beta1^t), p * (1 - lr * weight_decay)),  r = 1 / sqrt(1 - beta2^t)
+ * where 1 - beta^t is taken in binary64 and rounded once. Beside 8-bit states the
+ * root is the hardware's approximation (2^-23; 0 for a v' below 2^-126) and the quotient the product with its approximate
  * reciprocal (2^-23).
  * Parameters. FP32: p. BF16 with a master: p is the master, param = BF16(p'), to nearest even.
  * BF16 without one: p' is rounded stochastically, because an update is mostly far below half a
@@ -163,6 +163,8 @@ typedef struct {
  * Its high half is added to the 16 bits that a BF16 parameter drops; its low half to the upper
  * 16 of the 20 bits that a code of u drops.
  *   plan, chunks  as for nvfp4_grad_norm, of a list of optimizer tensors             (in)
+ *   state_bits  32 or 8, as the list's tensors have it (else NVFP4_ERR_VALUE; a list of the other
+ *              kind is left alone)
  *   control    device block; the kernel counts the step in it, so a captured call counts on at
  *              every replay                                                      (in/out)
  *   lr         finite, >= 0 (else NVFP4_ERR_VALUE); not used where lr_device is given
@@ -174,8 +176,8 @@ typedef struct {
  *              fake-quantization; zero-filled first in stream order; 0 for an empty tensor (out)
  *   count      number of tensors of the plan, for amax
  * Calls on one control block or one list must not overlap on the GPU. One kernel. */
-NVFP4_API nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, nvfp4_adamw_control* control, float lr,
-                                   const float* lr_device, double beta1, double beta2, float eps, uint32_t seed,
+NVFP4_API nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t state_bits,
+                                   nvfp4_adamw_control* control, float lr, const float* lr_device, double beta1, double beta2, float eps, uint32_t seed,
                                    const float* scale, float* amax, int64_t count, cudaStream_t stream);
 
 #ifdef __cplusplus

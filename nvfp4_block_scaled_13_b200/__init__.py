@@ -85,7 +85,7 @@ def load():
         L.nvfp4_layer_norm_backward.argtypes = [vp, vp, i32, vp, i32, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp]
         L.nvfp4_tensor_plan.argtypes = [vp, i64, vp, i64, vp]
         L.nvfp4_grad_norm.argtypes = [vp, i64, f32, vp, vp, vp, vp]
-        L.nvfp4_adamw.argtypes = [vp, i64, vp, f32, vp, f64, f64, f32, u32, vp, vp, i64, vp]
+        L.nvfp4_adamw.argtypes = [vp, i64, i32, vp, f32, vp, f64, f64, f32, u32, vp, vp, i64, vp]
         for f in (L.nvfp4_layer_norm, L.nvfp4_layer_norm_backward, L.nvfp4_tensor_plan, L.nvfp4_grad_norm, L.nvfp4_adamw):
             f.restype = i32
         L.nvfp4_layer_norm_workspace.argtypes, L.nvfp4_layer_norm_workspace.restype = [i64, i64], i64

@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/nvfp4_train.h"
@@ -27,9 +28,12 @@ constexpr int kThreads = 256;
 constexpr int kTile = kThreads * 8;        // elements of one pass of a CTA: eight a thread
 constexpr uint32_t kMagic = 0x4E56504Cu;
 constexpr uint32_t kGolden = 0x9E3779B9u;
+template <bool EIGHT>
+constexpr int kStepCtas = EIGHT ? 3 : 4;   // CTAs of an SM
+constexpr int kRingBytes = 66 * 1024;      // ring of each (8-bit states)
 constexpr int kMaxParts = 2048;            // CTAs of the gradient norm
 
-enum Kind : uint32_t { kGradients = 1, kOptimizer = 2 };
+enum Kind : uint32_t { kGradients = 1, kOptimizer32 = 2, kOptimizer8 = 3 };
 
 // The plan's image: Header, Tensor[count], Chunk[chunks]; every part a multiple of 16 bytes.
 struct Header {
@@ -39,7 +43,7 @@ struct Header {
 };
 struct Tensor {
     nvfp4_opt_tensor d;
-    uint32_t variant;   // Variant bits, and kVector when every pointer suits 16-byte accesses
+    uint32_t variant;   // kGradF32 and the others below
     uint32_t reserved[3];
 };
 struct Chunk {
@@ -47,7 +51,8 @@ struct Chunk {
 };
 static_assert(sizeof(Header) == 32 && sizeof(nvfp4_opt_tensor) == 88 && sizeof(Chunk) == 8, "plan layout");
 
-enum : uint32_t { kGradF32 = 1, kParamF32 = 2, kMaster = 4, kState8 = 8, kVector = 16 };
+// kVector: every pointer suits the step's whole accesses; kGradVector: the gradient the norm's.
+enum : uint32_t { kGradF32 = 1, kParamF32 = 2, kMaster = 4, kVector = 8, kGradVector = 16 };
 
 struct Image {
     const Header* header;
@@ -75,17 +80,6 @@ __device__ __forceinline__ void fetch8(const T* p, int64_t i, int64_t n, bool wh
         for (int j = 0; j < 8; ++j) v[j] = i + j < n ? to_float(p[i + j]) : 0.0f;
     }
 }
-template <typename T>
-__device__ __forceinline__ void put8(T* p, int64_t i, int64_t n, bool whole, const float (&v)[8]) {
-    if (whole) {
-        store8(p + i, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (i + j < n) p[i + j] = from_float<T>(v[j]);
-    }
-}
-
 // ---- 8-bit states --------------------------------------------------------------------------
 
 __device__ __forceinline__ float power_of_two(uint32_t biased) { return __uint_as_float(biased << 23); }
@@ -106,13 +100,27 @@ __device__ __forceinline__ void decode4(uint32_t codes, float2* out) {
 // maximum above 448 * 2^(s - 127) to the next power.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top) { return max((top + 0x1FFFFFu) >> 23, 9u) - 8u; }
 
-// The largest magnitude of a block, of which four threads hold eight elements each.
-__device__ __forceinline__ uint32_t block_top(const float2 (&v)[4]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top = max(top, max(magnitude(v[k].x), magnitude(v[k].y)));
+// The largest magnitude of a block, of which four threads hold eight elements each; NaN stays.
+__device__ __forceinline__ uint32_t join_block(uint32_t top) {
     top = max(top, __shfl_xor_sync(kFull, top, 1));
     return max(top, __shfl_xor_sync(kFull, top, 2));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t top_of(const float2 (&v)[4]) {
+    float top = max_nan(fabsf(v[0].x), fabsf(v[0].y));
+#pragma unroll
+    for (int k = 1; k < 4; ++k) top = max_nan(top, max_nan(fabsf(v[k].x), fabsf(v[k].y)));
+    return join_block(__float_as_uint(top));
+}
+__device__ __forceinline__ uint32_t top_of_positive(const float2 (&v)[4]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, max(__float_as_uint(v[k].x), __float_as_uint(v[k].y)));
+    return join_block(top);
 }
 
 __device__ __forceinline__ uint2 encode_nearest(const float2 (&v)[4], float inverse) {
@@ -211,31 +219,27 @@ struct StepArgs {
     uint32_t* amax;
 };
 
-// Root and quotient. 32-bit states take them as IEEE has them. Beside 8-bit states, whose step
-// is bound by the instructions, the hardware's approximations do (relative errors of at most 2^-23
-// each): u is then rounded to 4 bits, and the update is added to a parameter that it
-// changes in its last bits.
-template <bool EIGHT>
-__device__ __forceinline__ float root_of(float v) {
-    if (!EIGHT) return sqrtf(v);
+// Root and reciprocal beside 8-bit states, whose step is bound by the instructions: the hardware's
+// approximations (relative errors of at most 2^-23 each; a v below 2^-126 counts as 0). u is then
+// rounded to 4 bits, and the update is added to a parameter that it changes in its last bits.
+__device__ __forceinline__ float approximate_root(float v) {
     float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-template <bool EIGHT>
-__device__ __forceinline__ float quotient(float a, float b) {
-    if (!EIGHT) return a / b;
+__device__ __forceinline__ float approximate_reciprocal(float v) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(b));
-    return a * r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// Rounds to BF16 with the high half of each element's random word added to the dropped bits.
-__device__ __forceinline__ uint4 round_stochastic(const float2 (&p)[4], uint32_t word) {
-    uint32_t w[4];
+// Rounds four elements to BF16 with the high half of each element's random word (the first has
+// `word`) added to the dropped bits.
+__device__ __forceinline__ uint2 round_stochastic(const float2* p, uint32_t word) {
+    uint32_t w[2];
     float2 finite = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
         const uint32_t a = __float_as_uint(p[k].x) + ((word + 2 * k * kGolden) >> 16);
         const uint32_t b = __float_as_uint(p[k].y) + ((word + (2 * k + 1) * kGolden) >> 16);
         w[k] = __byte_perm(a, b, 0x7632);
@@ -244,26 +248,69 @@ __device__ __forceinline__ uint4 round_stochastic(const float2 (&p)[4], uint32_t
     // NaN and infinity are left to the conversion: adding to their bits could carry into the sign.
     if (!(finite.x + finite.y == 0.0f)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             if (!(fabsf(p[k].x) < INFINITY)) w[k] = (w[k] & 0xFFFF0000u) | to_bf16(p[k].x);
             if (!(fabsf(p[k].y) < INFINITY)) w[k] = (w[k] & 0xFFFFu) | (uint32_t(to_bf16(p[k].y)) << 16);
         }
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint2(w[0], w[1]);
 }
 
+// Joins two stored BF16 parameters, elements i and i + 1 of n (whole: both exist), to a maximum of magnitudes: two
+// halves side by side (NaN stays).
+__device__ __forceinline__ void join_stored(uint32_t& top, uint32_t w, bool whole, int64_t i, int64_t n) {
+    if (!whole && i + 1 >= n) w = i >= n ? 0u : w & 0xFFFFu;
+    asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %1;\n\tmax.NaN.bf16x2 %0, %0, m;\n\t}" : "+r"(top) : "r"(w));
+}
+
+// ---- a thread's eight elements -------------------------------------------------------------------
+
 template <typename T>
-__device__ __forceinline__ void fetch_pairs(const T* p, int64_t i, int64_t n, bool whole, float2 (&v)[4]) {
-    float f[8];
-    fetch8(p, i, n, whole, f);
+struct Eight {   // as they lie in memory
+    uint4 w[sizeof(T) / 2];
+};
+
+__device__ __forceinline__ void unpack(const Eight<bf16>& e, float2 (&v)[4]) {
+    const uint32_t a[4] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = make_float2(f[2 * k], f[2 * k + 1]);
+    for (int k = 0; k < 4; ++k) v[k] = make_float2(bf16_lo(a[k]), bf16_hi(a[k]));
 }
-__device__ __forceinline__ void put_pairs(float* p, int64_t i, int64_t n, bool whole, const float2 (&v)[4]) {
-    const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-    put8(p, i, n, whole, f);
+__device__ __forceinline__ void unpack(const Eight<float>& e, float2 (&v)[4]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        v[2 * k] = make_float2(__uint_as_float(e.w[k].x), __uint_as_float(e.w[k].y));
+        v[2 * k + 1] = make_float2(__uint_as_float(e.w[k].z), __uint_as_float(e.w[k].w));
+    }
 }
-__device__ __forceinline__ void put_bf16(bf16* p, int64_t i, int64_t n, bool whole, const uint4& w) {
+// whole: all eight exist and lie on a boundary of their own size (32 bytes in FP32, one access).
+__device__ __forceinline__ void fetch(const bf16* p, int64_t i, int64_t n, bool whole, Eight<bf16>& e) {
+    if (whole) {
+        e.w[0] = *reinterpret_cast<const uint4*>(p + i);
+    } else {
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) w[j / 2] |= uint32_t(p[i + j].bits) << (16 * (j & 1));
+        e.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void fetch(const float* p, int64_t i, int64_t n, bool whole, Eight<float>& e) {
+    if (whole) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(e.w[0].x), "=r"(e.w[0].y), "=r"(e.w[0].z), "=r"(e.w[0].w), "=r"(e.w[1].x), "=r"(e.w[1].y), "=r"(e.w[1].z),
+                       "=r"(e.w[1].w)
+                     : "l"(p + i)
+                     : "memory");
+    } else {
+        uint32_t w[8] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) w[j] = __float_as_uint(p[i + j]);
+        e.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        e.w[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+__device__ __forceinline__ void put(bf16* p, int64_t i, int64_t n, bool whole, const uint4& w) {
     if (whole) {
         *reinterpret_cast<uint4*>(p + i) = w;
     } else {
@@ -273,124 +320,367 @@ __device__ __forceinline__ void put_bf16(bf16* p, int64_t i, int64_t n, bool who
             if (i + j < n) p[i + j].bits = static_cast<uint16_t>(a[j / 2] >> (16 * (j & 1)));
     }
 }
-
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-// One chunk; the maximum of the stored parameters is joined to `top`.
-template <uint32_t KIND>
-__device__ __forceinline__ void step_chunk(const Tensor& t, int64_t lo, int64_t hi, const Factors& f, uint32_t& top) {
-    constexpr bool GRAD_F32 = KIND & kGradF32, PARAM_F32 = KIND & kParamF32, MASTER = KIND & kMaster, EIGHT = KIND & kState8;
-    const int64_t n = t.d.numel;
-    const float keep = 1.0f - t.d.weight_decay * f.lr;
-    for (int64_t base = lo; base < hi; base += kTile) {
-        const int64_t i = base + threadIdx.x * 8;
-        const bool whole = (t.variant & kVector) && i + 8 <= n;
-        float2 g[4], p[4], m[4], u[4];
-        if (GRAD_F32) {
-            fetch_pairs(static_cast<const float*>(t.d.grad), i, n, whole, g);
-        } else {
-            fetch_pairs(static_cast<const bf16*>(t.d.grad), i, n, whole, g);
-        }
-        if (MASTER) {
-            fetch_pairs(t.d.master, i, n, whole, p);
-        } else if (PARAM_F32) {
-            fetch_pairs(static_cast<const float*>(t.d.param), i, n, whole, p);
-        } else {
-            fetch_pairs(static_cast<const bf16*>(t.d.param), i, n, whole, p);
-        }
-        float sm = 0.0f, su = 0.0f;
-        if (EIGHT) {
-            uint2 cm, cu;
-            fetch_codes(static_cast<const uint8_t*>(t.d.exp_avg), i, n, whole, cm);
-            fetch_codes(static_cast<const uint8_t*>(t.d.exp_avg_sq), i, n, whole, cu);
-            if (i < n) {
-                sm = power_of_two(t.d.exp_avg_scale[i >> 5]);
-                su = power_of_two(t.d.exp_avg_sq_scale[i >> 5]);
-            }
-            decode4(cm.x, m);
-            decode4(cm.y, m + 2);
-            decode4(cu.x, u);
-            decode4(cu.y, u + 2);
-        } else {
-            fetch_pairs(static_cast<const float*>(t.d.exp_avg), i, n, whole, m);
-            fetch_pairs(static_cast<const float*>(t.d.exp_avg_sq), i, n, whole, u);
-        }
+__device__ __forceinline__ void put(float* p, int64_t i, int64_t n, bool whole, const float2 (&v)[4]) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + i), "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y),
+                     "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
+                     : "memory");
+    } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            g[k] = mul2(g[k], both(f.scale));
-            if (EIGHT) {
-                m[k] = mul2(m[k], both(sm));
-                u[k] = mul2(u[k], both(su));
-                u[k] = mul2(u[k], u[k]);
-            }
-            m[k] = fma2(m[k], both(f.beta1), mul2(g[k], both(f.rest1)));
-            u[k] = fma2(u[k], both(f.beta2), mul2(mul2(g[k], g[k]), both(f.rest2)));
-            const float2 root = make_float2(root_of<EIGHT>(u[k].x), root_of<EIGHT>(u[k].y));
-            const float2 under = fma2(root, both(f.root), both(f.eps));
-            const float2 ratio = make_float2(quotient<EIGHT>(m[k].x, under.x), quotient<EIGHT>(m[k].y, under.y));
-            p[k] = fma2(ratio, both(-f.rate), mul2(p[k], both(keep)));
-            if (EIGHT) u[k] = root;
-        }
-        const uint32_t word = mix(static_cast<uint32_t>((t.d.first + i) >> 3) ^ f.key);
-        if (PARAM_F32) {
-            put_pairs(static_cast<float*>(t.d.param), i, n, whole, p);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (i + 2 * k < n) top = max(top, magnitude(p[k].x));
-                if (i + 2 * k + 1 < n) top = max(top, magnitude(p[k].y));
-            }
-        } else {
-            uint4 w;
-            if (MASTER) {
-                put_pairs(t.d.master, i, n, whole, p);
-                w = make_uint4(to_bf16x2(p[0].x, p[0].y), to_bf16x2(p[1].x, p[1].y), to_bf16x2(p[2].x, p[2].y), to_bf16x2(p[3].x, p[3].y));
-            } else {
-                w = round_stochastic(p, word);
-            }
-            put_bf16(static_cast<bf16*>(t.d.param), i, n, whole, w);
-            uint32_t best = 0;   // of two halves
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t v = a[k];
-                if (i + 2 * k + 1 >= n) v = i + 2 * k >= n ? 0u : v & 0xFFFFu;
-                asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %1;\n\tmax.NaN.bf16x2 %0, %0, m;\n\t}" : "+r"(best) : "r"(v));
-            }
-            top = max(top, max(best << 16, best & 0xFFFF0000u));
-        }
-        if (EIGHT) {
-            const uint32_t tm = block_top(m), tu = block_top(u);
-            const uint32_t bm = scale_byte(tm), bu = scale_byte(tu);
-            put_codes(static_cast<uint8_t*>(t.d.exp_avg), i, n, whole, encode_nearest(m, power_of_two(254u - bm)));
-            put_codes(static_cast<uint8_t*>(t.d.exp_avg_sq), i, n, whole, encode_stochastic(u, power_of_two(254u - bu), word, tu));
-            if ((threadIdx.x & 3) == 0 && i < n) {
-                t.d.exp_avg_scale[i >> 5] = static_cast<uint8_t>(bm);
-                t.d.exp_avg_sq_scale[i >> 5] = static_cast<uint8_t>(bu);
-            }
-        } else {
-            put_pairs(static_cast<float*>(t.d.exp_avg), i, n, whole, m);
-            put_pairs(static_cast<float*>(t.d.exp_avg_sq), i, n, whole, u);
+            if (i + 2 * k < n) p[i + 2 * k] = v[k].x;
+            if (i + 2 * k + 1 < n) p[i + 2 * k + 1] = v[k].y;
         }
     }
 }
 
-// A step that does not take place still reports the parameters' maxima.
-__device__ __forceinline__ void top_of_chunk(const Tensor& t, int64_t lo, int64_t hi, uint32_t& top) {
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
-        top = max(top, magnitude((t.variant & kParamF32) ? static_cast<const float*>(t.d.param)[i]
-                                                         : to_float(static_cast<const bf16*>(t.d.param)[i])));
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <bool F32>
+using Float = typename std::conditional<F32, float, bf16>::type;
+
+// ---- 32-bit states ---------------------------------------------------------------------------------
+//
+// Four consecutive elements make a unit: 16 bytes in FP32, so that a warp's accesses are
+// contiguous. A thread has two units of a tile, all of whose reads are in flight together; with
+// 224 to 256 bytes a thread nothing more is needed to keep memory busy.
+
+struct Four {
+    float2 v[2];
+};
+
+__device__ __forceinline__ void read_four(const float* p, int64_t i, int64_t n, bool whole, Four& f) {
+    if (whole) {
+        const float4 a = *reinterpret_cast<const float4*>(p + i);
+        f.v[0] = make_float2(a.x, a.y);
+        f.v[1] = make_float2(a.z, a.w);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            f.v[k] = make_float2(i + 2 * k < n ? p[i + 2 * k] : 0.0f, i + 2 * k + 1 < n ? p[i + 2 * k + 1] : 0.0f);
+    }
+}
+__device__ __forceinline__ void read_four(const bf16* p, int64_t i, int64_t n, bool whole, Four& f) {
+    if (whole) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p + i);
+        f.v[0] = make_float2(bf16_lo(a.x), bf16_hi(a.x));
+        f.v[1] = make_float2(bf16_lo(a.y), bf16_hi(a.y));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            f.v[k] = make_float2(i + 2 * k < n ? to_float(p[i + 2 * k]) : 0.0f, i + 2 * k + 1 < n ? to_float(p[i + 2 * k + 1]) : 0.0f);
+    }
+}
+__device__ __forceinline__ void write_four(float* p, int64_t i, int64_t n, bool whole, const Four& f) {
+    if (whole) {
+        *reinterpret_cast<float4*>(p + i) = make_float4(f.v[0].x, f.v[0].y, f.v[1].x, f.v[1].y);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (i + 2 * k < n) p[i + 2 * k] = f.v[k].x;
+            if (i + 2 * k + 1 < n) p[i + 2 * k + 1] = f.v[k].y;
+        }
+    }
+}
+__device__ __forceinline__ void write_four(bf16* p, int64_t i, int64_t n, bool whole, uint2 w) {
+    if (whole) {
+        *reinterpret_cast<uint2*>(p + i) = w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) p[i + j].bits = static_cast<uint16_t>((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
+    }
 }
 
-__device__ __forceinline__ void publish_top(uint32_t& top, uint32_t* amax) {
+// A tile that WHOLE says to be all there, on whole accesses; otherwise one in which the tensor ends
+// or whose pointers do not suit. The first reads everything before it waits for anything.
+template <uint32_t KIND, bool WHOLE>
+__device__ __forceinline__ void step_tile_32(const nvfp4_opt_tensor& d, bool vector, int64_t base, float keep, const Factors& f,
+                                             uint32_t& top) {
+    constexpr bool PARAM_F32 = KIND & kParamF32, MASTER = KIND & kMaster;
+    using G = Float<(KIND & kGradF32) != 0>;
+    using P = Float<(KIND & (kParamF32 | kMaster)) != 0>;
+    P* source = static_cast<P*>(MASTER ? d.master : d.param);
+    float *exp_avg = static_cast<float*>(d.exp_avg), *exp_avg_sq = static_cast<float*>(d.exp_avg_sq);
+    const int64_t n = d.numel;
+    const int64_t at[2] = {base + threadIdx.x * 4, base + kTile / 2 + threadIdx.x * 4};
+    Four g[2], p[2], m[2], u[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool whole = WHOLE || (vector && at[h] + 4 <= n);
+        read_four(static_cast<const G*>(d.grad), at[h], n, whole, g[h]);
+        read_four(source, at[h], n, whole, p[h]);
+        read_four(exp_avg, at[h], n, whole, m[h]);
+        read_four(exp_avg_sq, at[h], n, whole, u[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t i = at[h];
+        const bool whole = WHOLE || (vector && i + 4 <= n);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float2 &gk = g[h].v[k], &mk = m[h].v[k], &uk = u[h].v[k];
+            gk = mul2(gk, both(f.scale));
+            mk = fma2(mk, both(f.beta1), mul2(gk, both(f.rest1)));
+            uk = fma2(uk, both(f.beta2), mul2(mul2(gk, gk), both(f.rest2)));
+            const float2 under = fma2(make_float2(sqrtf(uk.x), sqrtf(uk.y)), both(f.root), both(f.eps));
+            const float2 ratio = make_float2(mk.x / under.x, mk.y / under.y);
+            p[h].v[k] = fma2(ratio, both(-f.rate), mul2(p[h].v[k], both(keep)));
+        }
+        write_four(exp_avg, i, n, whole, m[h]);
+        write_four(exp_avg_sq, i, n, whole, u[h]);
+        if constexpr (PARAM_F32) {
+            write_four(source, i, n, whole, p[h]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (whole || i + 2 * k < n) top = max(top, magnitude(p[h].v[k].x));
+                if (whole || i + 2 * k + 1 < n) top = max(top, magnitude(p[h].v[k].y));
+            }
+        } else {
+            uint2 w;
+            if constexpr (MASTER) {
+                write_four(source, i, n, whole, p[h]);
+                w = make_uint2(to_bf16x2(p[h].v[0].x, p[h].v[0].y), to_bf16x2(p[h].v[1].x, p[h].v[1].y));
+                write_four(static_cast<bf16*>(d.param), i, n, whole, w);
+            } else {
+                const uint32_t place = static_cast<uint32_t>((d.first + i) >> 2);
+                w = round_stochastic(p[h].v, mix((place >> 1) ^ f.key) + (place & 1u) * (4 * kGolden));
+                write_four(source, i, n, whole, w);
+            }
+            join_stored(top, w.x, whole, i, n);
+            join_stored(top, w.y, whole, i + 2, n);
+        }
+    }
+}
+
+template <uint32_t KIND>
+__device__ __forceinline__ void step_chunk_32(const nvfp4_opt_tensor& d, bool vector, int64_t lo, int64_t hi, const Factors& f,
+                                              uint32_t& top) {
+    const float keep = 1.0f - d.weight_decay * f.lr;
+    if (vector)
+        for (; lo + kTile <= hi; lo += kTile) step_tile_32<KIND, true>(d, true, lo, keep, f, top);
+    for (; lo < hi; lo += kTile) step_tile_32<KIND, false>(d, vector, lo, keep, f, top);
+}
+
+// ---- 8-bit states ----------------------------------------------------------------------------------
+//
+// What a thread reads of the streams of a tensor, eight elements of each, and the ring in shared
+// memory through which the tiles after the next one arrive: 50 bytes a thread are too few to keep
+// memory busy, and a second set does not fit into the registers. A warp copies (cp.async) and reads
+// its own 256 elements only, so the ring needs no barrier beyond the warp's.
+template <uint32_t KIND>
+struct Read {
+    using G = Float<(KIND & kGradF32) != 0>;
+    using P = Float<(KIND & (kParamF32 | kMaster)) != 0>;
+    // bytes of a stage, by stream
+    static constexpr uint32_t kG = 8 * sizeof(G) * kThreads, kP = 8 * sizeof(P) * kThreads, kS = 8 * kThreads;
+    static constexpr uint32_t kStage = kG + kP + 2 * kS + kThreads / 32 * 16;
+    static constexpr int kStages = kRingBytes / kStage < 4 ? kRingBytes / kStage : 4;
+    static_assert(kStages >= 2, "the ring holds two tiles");
+
+    Eight<G> g;
+    Eight<P> p;
+    uint2 cm, cu;             // codes
+    uint32_t sm, su;          // scale bytes
+
+    static __device__ __forceinline__ const P* source(const nvfp4_opt_tensor& d) {
+        return static_cast<const P*>((KIND & kMaster) ? d.master : d.param);
+    }
+    // Without the ring: element by element unless all eight are whole.
+    __device__ __forceinline__ void fetch_from(const nvfp4_opt_tensor& d, int64_t i, bool whole) {
+        const int64_t n = d.numel;
+        fetch(static_cast<const G*>(d.grad), i, n, whole, g);
+        fetch(source(d), i, n, whole, p);
+        fetch_codes(static_cast<const uint8_t*>(d.exp_avg), i, n, whole, cm);
+        fetch_codes(static_cast<const uint8_t*>(d.exp_avg_sq), i, n, whole, cu);
+        sm = su = 0;
+        if (whole || i < n) {
+            sm = d.exp_avg_scale[i >> 5];
+            su = d.exp_avg_sq_scale[i >> 5];
+        }
+    }
+    // A warp's part of a stream, BYTES a lane, in contiguous accesses of 8 or 16 bytes a lane.
+    template <int BYTES>
+    static __device__ __forceinline__ void copy(uint32_t slot, const void* warp_from) {
+        const uint32_t to = slot + (threadIdx.x >> 5) * (32 * BYTES), lane = threadIdx.x & 31;
+        if (BYTES == 8) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + lane * 8), "l"(static_cast<const char*>(warp_from) + lane * 8)
+                         : "memory");
+        } else {
+#pragma unroll
+            for (int k = 0; k < BYTES / 16; ++k)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * 512 + lane * 16),
+                             "l"(static_cast<const char*>(warp_from) + k * 512 + lane * 16)
+                             : "memory");
+        }
+    }
+    template <typename T>
+    static __device__ __forceinline__ void take(uint32_t slot, Eight<T>& e) {
+#pragma unroll
+        for (int k = 0; k < int(sizeof(T)) / 2; ++k)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(e.w[k].x), "=r"(e.w[k].y), "=r"(e.w[k].z), "=r"(e.w[k].w)
+                         : "r"(slot + threadIdx.x * uint32_t(8 * sizeof(T)) + k * 16)
+                         : "memory");
+    }
+    static __device__ __forceinline__ void take(uint32_t slot, uint2& c) {
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(slot + threadIdx.x * 8) : "memory");
+    }
+    static __device__ __forceinline__ uint32_t take_byte(uint32_t from) {
+        uint16_t b;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=h"(b) : "r"(from) : "memory");
+        return b;
+    }
+    // `i`: the first element of the warp.
+    static __device__ __forceinline__ void start(const nvfp4_opt_tensor& d, int64_t i, uint32_t slot) {
+        copy<8 * sizeof(G)>(slot, static_cast<const G*>(d.grad) + i);
+        copy<8 * sizeof(P)>(slot + kG, source(d) + i);
+        copy<8>(slot + kG + kP, static_cast<const uint8_t*>(d.exp_avg) + i);
+        copy<8>(slot + kG + kP + kS, static_cast<const uint8_t*>(d.exp_avg_sq) + i);
+        const uint32_t lane = threadIdx.x & 31;   // lanes 0 and 1 copy the eight scale bytes of m, 2 and 3 those of u
+        if (lane < 4) {
+            const uint8_t* from = (lane < 2 ? d.exp_avg_scale : d.exp_avg_sq_scale) + (i >> 5) + (lane & 1) * 4;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot + kG + kP + 2 * kS + (threadIdx.x >> 5) * 16 + lane * 4),
+                         "l"(from)
+                         : "memory");
+        }
+    }
+    __device__ __forceinline__ void collect(uint32_t slot) {
+        take(slot, g);
+        take(slot + kG, p);
+        take(slot + kG + kP, cm);
+        take(slot + kG + kP + kS, cu);
+        const uint32_t bytes = slot + kG + kP + 2 * kS + (threadIdx.x >> 5) * 16 + ((threadIdx.x & 31) >> 2);
+        sm = take_byte(bytes);
+        su = take_byte(bytes + 8);
+    }
+};
+
+// The step of a thread's eight elements; the maximum of the stored parameters is joined to `top`.
+template <uint32_t KIND>
+__device__ __forceinline__ void step_eight(const nvfp4_opt_tensor& d, const Read<KIND>& r, int64_t i, bool whole, float keep,
+                                           const Factors& f, uint32_t& top) {
+    constexpr bool PARAM_F32 = KIND & kParamF32, MASTER = KIND & kMaster;
+    const int64_t n = d.numel;
+    float2 g[4], p[4], m[4], u[4];
+    unpack(r.g, g);
+    unpack(r.p, p);
+    decode4(r.cm.x, m);
+    decode4(r.cm.y, m + 2);
+    decode4(r.cu.x, u);
+    decode4(r.cu.y, u + 2);
+    const float sm = power_of_two(r.sm), su = power_of_two(r.su);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        g[k] = mul2(g[k], both(f.scale));
+        m[k] = fma2(mul2(m[k], both(sm)), both(f.beta1), mul2(g[k], both(f.rest1)));
+        u[k] = mul2(u[k], both(su));
+        u[k] = fma2(mul2(u[k], u[k]), both(f.beta2), mul2(mul2(g[k], g[k]), both(f.rest2)));
+        u[k] = make_float2(approximate_root(u[k].x), approximate_root(u[k].y));
+        const float2 under = fma2(u[k], both(f.root), both(f.eps));
+        const float2 ratio = mul2(m[k], make_float2(approximate_reciprocal(under.x), approximate_reciprocal(under.y)));
+        p[k] = fma2(ratio, both(-f.rate), mul2(p[k], both(keep)));
+    }
+    const uint32_t word = mix(static_cast<uint32_t>((d.first + i) >> 3) ^ f.key);
+    if constexpr (PARAM_F32) {
+        put(static_cast<float*>(d.param), i, n, whole, p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (whole || i + 2 * k < n) top = max(top, magnitude(p[k].x));
+            if (whole || i + 2 * k + 1 < n) top = max(top, magnitude(p[k].y));
+        }
+    } else {
+        uint4 w;
+        if constexpr (MASTER) {
+            put(d.master, i, n, whole, p);
+            w = make_uint4(to_bf16x2(p[0].x, p[0].y), to_bf16x2(p[1].x, p[1].y), to_bf16x2(p[2].x, p[2].y), to_bf16x2(p[3].x, p[3].y));
+        } else {
+            const uint2 a = round_stochastic(p, word), b = round_stochastic(p + 2, word + 4 * kGolden);
+            w = make_uint4(a.x, a.y, b.x, b.y);
+        }
+        put(static_cast<bf16*>(d.param), i, n, whole, w);
+        join_stored(top, w.x, whole, i, n);
+        join_stored(top, w.y, whole, i + 2, n);
+        join_stored(top, w.z, whole, i + 4, n);
+        join_stored(top, w.w, whole, i + 6, n);
+    }
+    const uint32_t tm = top_of(m), tu = top_of_positive(u);
+    const uint32_t bm = scale_byte(tm), bu = scale_byte(tu);
+    put_codes(static_cast<uint8_t*>(d.exp_avg), i, n, whole, encode_nearest(m, power_of_two(254u - bm)));
+    put_codes(static_cast<uint8_t*>(d.exp_avg_sq), i, n, whole, encode_stochastic(u, power_of_two(254u - bu), word, tu));
+    if ((threadIdx.x & 3) == 0 && (whole || i < n)) {
+        d.exp_avg_scale[i >> 5] = static_cast<uint8_t>(bm);
+        d.exp_avg_sq_scale[i >> 5] = static_cast<uint8_t>(bu);
+    }
+}
+
+// Whole tiles through the ring, then the tile in which the tensor ends, or all of them where a
+// pointer does not suit whole accesses. A function of its own for each kind: inlined side by side,
+// the kinds took registers from one another and spilled.
+template <uint32_t KIND>
+__device__ __noinline__ uint32_t step_chunk_8(const nvfp4_opt_tensor& d, bool vector, int64_t lo, int64_t hi, const Factors& f,
+                                              uint32_t top) {
+    extern __shared__ uint4 ring[];
+    constexpr int S = Read<KIND>::kStages;
+    const float keep = 1.0f - d.weight_decay * f.lr;
+    const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const int ahead = (threadIdx.x & 31) * 8;   // elements of the warp before this thread's
+    int64_t at = lo + threadIdx.x * 8;
+    const int whole = vector ? static_cast<int>((hi - lo) / kTile) : 0;
+    __syncwarp();   // nothing of an earlier chunk is still being read by another lane
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) {
+        if (k < whole) Read<KIND>::start(d, at - ahead + k * kTile, slots + k * Read<KIND>::kStage);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int stage = 0;
+    for (int k = 0; k < whole; ++k, at += kTile) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncwarp();
+        Read<KIND> now;
+        now.collect(slots + stage * Read<KIND>::kStage);
+        const int behind = stage == 0 ? S - 1 : stage - 1;   // read by all lanes before the __syncwarp above
+        if (k + S - 1 < whole) Read<KIND>::start(d, at - ahead + (S - 1) * kTile, slots + behind * Read<KIND>::kStage);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        stage = stage == S - 1 ? 0 : stage + 1;
+        step_eight<KIND>(d, now, at, true, keep, f, top);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (; at - threadIdx.x * 8 < hi; at += kTile) {
+        Read<KIND> now;
+        const bool eight = vector && at + 8 <= d.numel;
+        now.fetch_from(d, at, eight);
+        step_eight<KIND>(d, now, at, eight, keep, f, top);
+    }
+    return top;
+}
+
+// A step that does not take place still reports the parameters' maxima.
+__device__ __forceinline__ void top_of_chunk(const Tensor& t, int64_t lo, int64_t hi, uint32_t& top) {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+        if (t.variant & kParamF32) {
+            top = max(top, magnitude(static_cast<const float*>(t.d.param)[i]));
+        } else {
+            join_stored(top, static_cast<const bf16*>(t.d.param)[i].bits, true, 0, 0);
+        }
+    }
+}
+
+// `top`: the bits of an FP32 magnitude, or the halves of two BF16 ones.
+__device__ __forceinline__ void publish_top(uint32_t& top, bool halves, uint32_t* amax) {
+    if (halves) top = max(top << 16, top & 0xFFFF0000u);
     const uint32_t best = __reduce_max_sync(kFull, top);
     if ((threadIdx.x & 31) == 0 && best != 0) atomicMax(amax, best);
     top = 0;
 }
 
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const StepArgs a) {
+template <bool EIGHT>
+__global__ void __launch_bounds__(kThreads, kStepCtas<EIGHT>) adamw_kernel(const StepArgs a) {
     __shared__ Factors shared;
+    __shared__ Tensor tensors[kThreads / 32];
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Image image = image_of(a.plan);
-    if (image.header->magic != kMagic || image.header->kind != kOptimizer) return;
+    if (image.header->magic != kMagic || image.header->kind != (EIGHT ? kOptimizer8 : kOptimizer32)) return;
     if (threadIdx.x == 0) {
         Factors f;
         f.beta1 = static_cast<float>(a.beta1);
@@ -399,44 +689,60 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const StepArgs a) {
         f.rest2 = static_cast<float>(1.0 - a.beta2);
         f.eps = a.eps;
         f.lr = a.lr_device ? *a.lr_device : a.lr;
-        f.rate = static_cast<float>(static_cast<double>(f.lr) / (1.0 - a.control->beta1_t * a.beta1));
-        f.root = static_cast<float>(1.0 / sqrt(1.0 - a.control->beta2_t * a.beta2));
+        f.rate = f.lr / static_cast<float>(1.0 - a.control->beta1_t * a.beta1);
+        f.root = 1.0f / sqrtf(static_cast<float>(1.0 - a.control->beta2_t * a.beta2));
         f.scale = a.scale ? *a.scale : 1.0f;
         f.key = mix(a.seed + kGolden * a.control->step);
         shared = f;
     }
     __syncthreads();
-    const Factors f = shared;
+    const Factors& f = shared;
     const bool takes_place = isfinite(f.scale);
     const uint32_t chunks = image.header->chunks;
     const int64_t length = image.header->chunk_elements;
     uint32_t top = 0, last = 0xFFFFFFFFu;
+    bool halves = false;
+    Chunk upcoming{};
+    if (blockIdx.x < chunks) upcoming = image.chunks[blockIdx.x];
     for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const Chunk chunk = image.chunks[c];
-        const Tensor& t = image.tensors[chunk.tensor];
-        if (a.amax && last != 0xFFFFFFFFu && last != chunk.tensor) publish_top(top, a.amax + last);
+        const Chunk chunk = upcoming;
+        if (c + gridDim.x < chunks) upcoming = image.chunks[c + gridDim.x];
+        // each warp keeps the tensor's description in shared memory: registers are scarce below
+        __syncwarp();
+        if (lane < sizeof(Tensor) / 4)
+            reinterpret_cast<uint32_t*>(&tensors[warp])[lane] = reinterpret_cast<const uint32_t*>(&image.tensors[chunk.tensor])[lane];
+        __syncwarp();
+        const Tensor& t = tensors[warp];
+        if (a.amax && last != 0xFFFFFFFFu && last != chunk.tensor) publish_top(top, halves, a.amax + last);
         last = chunk.tensor;
+        halves = !(t.variant & kParamF32);
         const int64_t lo = chunk.index * length, hi = min(t.d.numel, lo + length);
         if (!takes_place) {
             if (a.amax) top_of_chunk(t, lo, hi, top);
             continue;
         }
-        switch (t.variant & 15u) {
-            case 0: step_chunk<0>(t, lo, hi, f, top); break;
-            case kGradF32: step_chunk<kGradF32>(t, lo, hi, f, top); break;
-            case kParamF32: step_chunk<kParamF32>(t, lo, hi, f, top); break;
-            case kParamF32 | kGradF32: step_chunk<kParamF32 | kGradF32>(t, lo, hi, f, top); break;
-            case kMaster: step_chunk<kMaster>(t, lo, hi, f, top); break;
-            case kMaster | kGradF32: step_chunk<kMaster | kGradF32>(t, lo, hi, f, top); break;
-            case kState8: step_chunk<kState8>(t, lo, hi, f, top); break;
-            case kState8 | kGradF32: step_chunk<kState8 | kGradF32>(t, lo, hi, f, top); break;
-            case kState8 | kParamF32: step_chunk<kState8 | kParamF32>(t, lo, hi, f, top); break;
-            case kState8 | kParamF32 | kGradF32: step_chunk<kState8 | kParamF32 | kGradF32>(t, lo, hi, f, top); break;
-            case kState8 | kMaster: step_chunk<kState8 | kMaster>(t, lo, hi, f, top); break;
-            case kState8 | kMaster | kGradF32: step_chunk<kState8 | kMaster | kGradF32>(t, lo, hi, f, top); break;
+        const bool vector = t.variant & kVector;
+        if constexpr (EIGHT) {
+            switch (t.variant & (kGradF32 | kParamF32 | kMaster)) {
+                case 0: top = step_chunk_8<0>(t.d, vector, lo, hi, f, top); break;
+                case kGradF32: top = step_chunk_8<kGradF32>(t.d, vector, lo, hi, f, top); break;
+                case kParamF32: top = step_chunk_8<kParamF32>(t.d, vector, lo, hi, f, top); break;
+                case kParamF32 | kGradF32: top = step_chunk_8<kParamF32 | kGradF32>(t.d, vector, lo, hi, f, top); break;
+                case kMaster: top = step_chunk_8<kMaster>(t.d, vector, lo, hi, f, top); break;
+                default: top = step_chunk_8<kMaster | kGradF32>(t.d, vector, lo, hi, f, top); break;
+            }
+        } else {
+            switch (t.variant & (kGradF32 | kParamF32 | kMaster)) {
+                case 0: step_chunk_32<0>(t.d, vector, lo, hi, f, top); break;
+                case kGradF32: step_chunk_32<kGradF32>(t.d, vector, lo, hi, f, top); break;
+                case kParamF32: step_chunk_32<kParamF32>(t.d, vector, lo, hi, f, top); break;
+                case kParamF32 | kGradF32: step_chunk_32<kParamF32 | kGradF32>(t.d, vector, lo, hi, f, top); break;
+                case kMaster: step_chunk_32<kMaster>(t.d, vector, lo, hi, f, top); break;
+                default: step_chunk_32<kMaster | kGradF32>(t.d, vector, lo, hi, f, top); break;
+            }
         }
     }
-    if (a.amax && last != 0xFFFFFFFFu) publish_top(top, a.amax + last);
+    if (a.amax && last != 0xFFFFFFFFu) publish_top(top, halves, a.amax + last);
     // The last CTA to arrive counts the step: every CTA has read the control block before it
     // arrives.
     __syncthreads();
@@ -456,15 +762,19 @@ struct NormWorkspace {
 };
 static_assert(sizeof(NormWorkspace) == NVFP4_GRAD_NORM_WORKSPACE, "workspace size");
 
-__device__ __forceinline__ double sum_of_squares(const float (&g)[8]) {
-    float s = 0.0f;
+__device__ __forceinline__ double sum_of_squares(const float2 (&g)[4]) {
+    float2 s2 = mul2(g[0], g[0]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(g[j], g[j], s);
+    for (int k = 1; k < 4; ++k) s2 = fma2(g[k], g[k], s2);
+    const float s = s2.x + s2.y;
     // Outside this range a square may have overflowed or lost bits to underflow.
     if (!(s >= 0x1p-90f && s <= FLT_MAX)) {
         double d = 0.0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d = fma(static_cast<double>(g[j]), static_cast<double>(g[j]), d);
+        for (int k = 0; k < 4; ++k) {
+            d = fma(static_cast<double>(g[k].x), static_cast<double>(g[k].x), d);
+            d = fma(static_cast<double>(g[k].y), static_cast<double>(g[k].y), d);
+        }
         return d;
     }
     return static_cast<double>(s);
@@ -490,10 +800,12 @@ template <typename T>
 __device__ __forceinline__ double norm_chunk(const Tensor& t, int64_t lo, int64_t hi) {
     double sum = 0.0;
     const T* g = static_cast<const T*>(t.d.grad);
-    const bool vector = t.variant & kVector;
+    const bool vector = t.variant & kGradVector;
     for (int64_t i = lo + threadIdx.x * 8; i < hi; i += kTile) {
-        float v[8];
-        fetch8(g, i, t.d.numel, vector && i + 8 <= t.d.numel, v);
+        Eight<T> e;
+        float2 v[4];
+        fetch(g, i, t.d.numel, vector && i + 8 <= t.d.numel, e);
+        unpack(e, v);
         sum += sum_of_squares(v);
     }
     return sum;
@@ -544,10 +856,10 @@ nvfp4_status launched() { return cudaGetLastError() == cudaSuccess ? NVFP4_OK : 
 constexpr int64_t kMostElements = int64_t(1) << 34;
 constexpr int64_t kMostTensors = int64_t(1) << 24;
 
-// Elements of a chunk: eight tiles where the list is long enough for every CTA to get several such
+// Elements of a chunk: sixteen tiles where the list is long enough for every CTA to get several such
 // chunks, fewer for shorter lists, so that they still spread over the SMs.
 int64_t chunk_elements(int64_t total) {
-    int64_t tiles = 8;
+    int64_t tiles = 16;
     while (tiles > 1 && total < tiles * kTile * 4096) tiles /= 2;
     return tiles * kTile;
 }
@@ -614,6 +926,22 @@ unsigned resident_grid(int64_t chunks, int per_sm) {
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(chunks, int64_t(sm_count()) * per_sm)));
 }
 
+// Lets the step's kernel have its ring on the current device (once per device).
+bool allow_ring() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> allowed[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+    if (dev < kMaxDevices && allowed[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(adamw_kernel<true>), cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (dev < kMaxDevices) allowed[dev].store(true, std::memory_order_release);
+    return true;
+}
+
 }  // namespace
 
 extern "C" int64_t nvfp4_tensor_plan_bytes(const nvfp4_opt_tensor* tensors, int64_t count) {
@@ -630,6 +958,7 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
     bool gradients = true;   // tensors without an element say nothing
     for (int64_t i = 0; i < count; ++i)
         if (tensors[i].param != nullptr) gradients = false;
+    int32_t bits = 0;
     std::vector<Span> spans;
     try {
         for (int64_t i = 0; i < count; ++i) {
@@ -643,6 +972,8 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
             };
             add(t.grad, t.numel * size_of(t.grad_type), false);
             if (gradients) continue;
+            if (bits != 0 && bits != t.state_bits) return NVFP4_ERR_VALUE;
+            bits = t.state_bits;
             add(t.param, t.numel * size_of(t.param_type), true);
             add(t.master, t.numel * 4, true);
             add(t.exp_avg, t.numel * t.state_bits / 8, true);
@@ -660,7 +991,7 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
     char* out = static_cast<char*>(image);
     Header header{};
     header.magic = kMagic;
-    header.kind = gradients ? kGradients : kOptimizer;
+    header.kind = gradients ? kGradients : bits == 8 ? kOptimizer8 : kOptimizer32;
     header.count = static_cast<uint32_t>(count);
     header.chunks = static_cast<uint32_t>(chunks);
     header.chunk_elements = static_cast<uint32_t>(length);
@@ -669,14 +1000,15 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
     for (int64_t i = 0; i < count; ++i) {
         Tensor t{};
         t.d = tensors[i];
-        if (gradients) {
-            t.variant = (t.d.grad_type == NVFP4_TYPE_F32 ? kGradF32 : 0u) | (aligned_to(t.d.grad, 16) ? kVector : 0u);
-        } else {
-            const uintptr_t state = t.d.state_bits == 32 ? 16 : 8;
-            t.variant = (t.d.grad_type == NVFP4_TYPE_F32 ? kGradF32 : 0u) | (t.d.param_type == NVFP4_TYPE_F32 ? kParamF32 : 0u) |
-                        (t.d.master ? kMaster : 0u) | (t.d.state_bits == 8 ? kState8 : 0u);
-            if (aligned_to(t.d.grad, 16) && aligned_to(t.d.param, 16) && aligned_to(t.d.master, 16) &&
-                aligned_to(t.d.exp_avg, state) && aligned_to(t.d.exp_avg_sq, state))
+        t.variant = (t.d.grad_type == NVFP4_TYPE_F32 ? kGradF32 : 0u) | (aligned_to(t.d.grad, 8 * size_of(t.d.grad_type)) ? kGradVector : 0u);
+        if (!gradients) {
+            t.variant |= (t.d.param_type == NVFP4_TYPE_F32 ? kParamF32 : 0u) | (t.d.master ? kMaster : 0u);
+            // whole accesses: of eight elements beside 8-bit states, of four beside 32-bit ones
+            const int unit = t.d.state_bits == 8 ? 8 : 4, state = t.d.state_bits == 8 ? 1 : 4;
+            const auto suits = [&](const void* p, int64_t element) { return aligned_to(p, unit * element); };
+            if (suits(t.d.grad, size_of(t.d.grad_type)) && suits(t.d.param, size_of(t.d.param_type)) && suits(t.d.master, 4) &&
+                suits(t.d.exp_avg, state) && suits(t.d.exp_avg_sq, state) &&
+                (state == 4 || (aligned_to(t.d.exp_avg_scale, 4) && aligned_to(t.d.exp_avg_sq_scale, 4))))
                 t.variant |= kVector;
         }
         memcpy(out + tensor_offset() + sizeof(Tensor) * i, &t, sizeof t);
@@ -701,12 +1033,12 @@ extern "C" nvfp4_status nvfp4_grad_norm(const void* plan, int64_t chunks, float 
     return launched();
 }
 
-extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, nvfp4_adamw_control* control, float lr,
+extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t state_bits, nvfp4_adamw_control* control, float lr,
                                     const float* lr_device, double beta1, double beta2, float eps, uint32_t seed,
                                     const float* scale, float* amax, int64_t count, cudaStream_t stream) {
     if (plan == nullptr || control == nullptr) return NVFP4_ERR_NULL;
     if (chunks < 0 || count < 0) return NVFP4_ERR_SHAPE;
-    if ((lr_device == nullptr && !(lr >= 0.0f && lr <= FLT_MAX)) || !(beta1 >= 0.0 && beta1 < 1.0) ||
+    if ((state_bits != 32 && state_bits != 8) || (lr_device == nullptr && !(lr >= 0.0f && lr <= FLT_MAX)) || !(beta1 >= 0.0 && beta1 < 1.0) ||
         !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0f && eps <= FLT_MAX))
         return NVFP4_ERR_VALUE;
     if (!aligned_to(plan, 16) || !aligned_to(control, 8) || !aligned_to(lr_device, 4) || !aligned_to(scale, 4) ||
@@ -715,6 +1047,11 @@ extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, nvfp4_adam
     if (amax && count > 0 && cudaMemsetAsync(amax, 0, static_cast<size_t>(count) * 4, stream) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     const StepArgs a{plan, control, lr, lr_device, beta1, beta2, eps, seed, scale, reinterpret_cast<uint32_t*>(amax)};
-    adamw_kernel<<<resident_grid(chunks, 4), kThreads, 0, stream>>>(a);
+    if (state_bits == 32) {
+        adamw_kernel<false><<<resident_grid(chunks, kStepCtas<false>), kThreads, 0, stream>>>(a);
+    } else {
+        if (!allow_ring()) return NVFP4_ERR_CUDA;
+        adamw_kernel<true><<<resident_grid(chunks, kStepCtas<true>), kThreads, kRingBytes, stream>>>(a);
+    }
     return launched();
 }

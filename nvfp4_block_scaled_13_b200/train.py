@@ -72,9 +72,9 @@ def nvfp4_grad_norm(plan, chunks, max_norm, norm, scale, workspace, stream=None)
                                   _stream(stream)), "nvfp4_grad_norm")
 
 
-def nvfp4_adamw(plan, chunks, control, lr, lr_device, beta1, beta2, eps, seed, scale=None, amax=None, count=0,
+def nvfp4_adamw(plan, chunks, state_bits, control, lr, lr_device, beta1, beta2, eps, seed, scale=None, amax=None, count=0,
                 stream=None):
-    _check(load().nvfp4_adamw(_ptr(plan), chunks, _ptr(control), lr, _ptr(lr_device), beta1, beta2, eps, seed,
+    _check(load().nvfp4_adamw(_ptr(plan), chunks, state_bits, _ptr(control), lr, _ptr(lr_device), beta1, beta2, eps, seed,
                               _ptr(scale), _ptr(amax), count, _stream(stream)), "nvfp4_adamw")
 
 
@@ -389,5 +389,5 @@ def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
     if scale is not None:
         _same(scale, plan.control, (1,), "scale", torch.float32)
     with _on(plan.device):
-        nvfp4_adamw(plan.table, plan.chunks, plan.control, lr, lr_device, plan.betas[0], plan.betas[1], plan.eps, plan.seed,
+        nvfp4_adamw(plan.table, plan.chunks, plan.state_bits, plan.control, lr, lr_device, plan.betas[0], plan.betas[1], plan.eps, plan.seed,
                     scale, plan.amax, plan.count if plan.amax is not None else 0, stream)

@@ -76,22 +76,23 @@ def test_library_exports_the_header_and_the_binding_mirrors_it():
     (lambda L: L.nvfp4_grad_norm(A + 8, 1, 1.0, A, A, A, None), 3),
     (lambda L: L.nvfp4_grad_norm(A, 1, 1.0, A + 2, A, A, None), 3),
     (lambda L: L.nvfp4_grad_norm(A, 1, 1.0, A, A, A + 8, None), 3),
-    # nvfp4_adamw(plan, chunks, control, lr, lr_device, beta1, beta2, eps, seed, scale, amax, count, stream)
-    (lambda L: L.nvfp4_adamw(None, 1, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 1),
-    (lambda L: L.nvfp4_adamw(A, 1, None, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 1),
-    (lambda L: L.nvfp4_adamw(A, -1, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 2),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, A, -1, None), 2),
-    (lambda L: L.nvfp4_adamw(A, 1, A, -1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 7),
-    (lambda L: L.nvfp4_adamw(A, 1, A, INF, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 7),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, None, 1.0, 0.99, 1e-8, 0, None, None, 0, None), 7),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, None, 0.9, -0.1, 1e-8, 0, None, None, 0, None), 7),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, None, 0.9, NAN, 1e-8, 0, None, None, 0, None), 7),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, None, 0.9, 0.99, -1.0, 0, None, None, 0, None), 7),
-    (lambda L: L.nvfp4_adamw(A + 8, 1, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 3),
-    (lambda L: L.nvfp4_adamw(A, 1, A + 4, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 3),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, A + 2, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 3),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, A + 1, None, 0, None), 3),
-    (lambda L: L.nvfp4_adamw(A, 1, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, A + 2, 1, None), 3),
+    # nvfp4_adamw(plan, chunks, state_bits, control, lr, lr_device, beta1, beta2, eps, seed, scale, amax, count, stream)
+    (lambda L: L.nvfp4_adamw(A, 1, 16, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 7),
+    (lambda L: L.nvfp4_adamw(None, 1, 32, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 1),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, None, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 1),
+    (lambda L: L.nvfp4_adamw(A, -1, 32, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 2),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, A, -1, None), 2),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, -1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 7),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, INF, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 7),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, None, 1.0, 0.99, 1e-8, 0, None, None, 0, None), 7),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, None, 0.9, -0.1, 1e-8, 0, None, None, 0, None), 7),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, None, 0.9, NAN, 1e-8, 0, None, None, 0, None), 7),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, None, 0.9, 0.99, -1.0, 0, None, None, 0, None), 7),
+    (lambda L: L.nvfp4_adamw(A + 8, 1, 32, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 3),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A + 4, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 3),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, A + 2, 0.9, 0.99, 1e-8, 0, None, None, 0, None), 3),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, A + 1, None, 0, None), 3),
+    (lambda L: L.nvfp4_adamw(A, 1, 32, A, 1e-3, None, 0.9, 0.99, 1e-8, 0, None, A + 2, 1, None), 3),
 ])
 def test_invalid_arguments_rejected_on_host(call, expected):
     assert call(nv.load()) == expected
@@ -173,6 +174,7 @@ def test_plan_of_gradients_alone():
     ([tensor(weight_decay=NAN)], 7),
     ([tensor(param_type=1, master=9 << 24)], 7),
     ([tensor(), nv.OptTensor(grad=1 << 40, numel=8)], 7),            # both kinds in one list
+    ([tensor(), tensor(at=1 << 40, state_bits=8, exp_avg_scale=1 << 30, exp_avg_sq_scale=1 << 31)], 7),   # both kinds of state
     ([tensor(), tensor()], 7),                                         # the same tensor twice
     ([tensor(), tensor(at=A + 64)], 7),                               # overlapping parameters
     ([tensor(grad=A)], 7),                                             # a gradient over its parameter

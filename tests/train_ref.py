@@ -116,8 +116,8 @@ def adamw_bits(p, g, m, v, *, param_bf16, master, bits, lr, decay, betas, eps, s
     n = len(p)
     lr = f(lr)
     b1, r1, b2, r2 = f(betas[0]), f(1.0 - betas[0]), f(betas[1]), f(1.0 - betas[1])
-    rate = f(np.float64(lr) / (1.0 - np.float64(betas[0]) ** steps * betas[0]))
-    root_factor = f(1.0 / np.sqrt(1.0 - np.float64(betas[1]) ** steps * betas[1]))
+    rate = lr / f(1.0 - np.float64(betas[0]) ** steps * betas[0])
+    root_factor = f(1) / np.sqrt(f(1.0 - np.float64(betas[1]) ** steps * betas[1]))
     keep = f(1.0) - f(decay) * lr
     g = g.astype(f) * f(scale)
     if bits == 8:
@@ -126,6 +126,8 @@ def adamw_bits(p, g, m, v, *, param_bf16, master, bits, lr, decay, betas, eps, s
     m = fma(m, b1, g * r1)
     v = fma(v, b2, (g * g) * r2)
     root = np.sqrt(v)
+    if bits == 8:
+        root = np.where(v < f(2.0 ** -126), f(0), root)
     ratio = m / fma(root, root_factor, f(eps))
     q = fma(ratio, -rate, p * keep)
     assert m.dtype == v.dtype == q.dtype == np.float32
