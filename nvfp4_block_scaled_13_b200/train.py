@@ -78,52 +78,60 @@ def nvfp4_adamw(plan, chunks, state_bits, control, lr, lr_device, beta1, beta2, 
                               _ptr(scale), _ptr(amax), count, _stream(stream)), "nvfp4_adamw")
 
 
-# ---- checks shared by the wrappers ---------------------------------------------------------------
+# ---- what the wrappers share ---------------------------------------------------------------------
+#
+# A step calls these operators many times on small tensors, where the host's part of a call is what
+# counts: torch is looked up once, and a stream is taken as a number.
 
-def _type_of(t, what):
+_torch = None
+_types = {}
+_HERE = contextlib.nullcontext()
+
+
+def _load_torch():
+    global _torch, _types
     import torch
 
-    if t.dtype == torch.bfloat16:
-        return TYPE_BF16
-    if t.dtype == torch.float32:
-        return TYPE_F32
-    raise ValueError(f"nvfp4: {what} must be BF16 or FP32, not {t.dtype}")
+    _types = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+    _torch = torch
+    return torch
+
+
+def _type_of(t, what):
+    code = _types.get(t.dtype)
+    if code is None:
+        raise ValueError(f"nvfp4: {what} must be BF16 or FP32, not {t.dtype}")
+    return code
 
 
 def _on(device):
     """A context in which `device` is current."""
-    import torch
+    return _HERE if _torch._C._cuda_getDevice() == device.index else _torch.cuda.device(device)
 
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+def _raw(stream, device):
+    """The stream as a number; None: the current one of `device`."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _lend(stream, *tensors):
     """Memory that torch's current stream allocated and `stream` works on is kept until that work is done."""
-    import torch
-
-    if stream is None:
-        return
-    current = torch.cuda.current_stream(tensors[0].device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream, device=tensors[0].device)
-    if stream.cuda_stream != current.cuda_stream:
-        for t in tensors:
+    given = [t for t in tensors if t is not None]
+    device = given[0].device
+    raw = _raw(stream, device)
+    if raw != _raw(None, device):
+        if isinstance(stream, int):
+            stream = _torch.cuda.ExternalStream(stream, device=device)
+        for t in given:
             t.record_stream(stream)
-
-
-def _rows_cols(x, what):
-    if not x.is_cuda:
-        raise ValueError("nvfp4: tensors must live on a CUDA device")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"{what}: x must have a last dimension of at least 1")
-    cols = x.shape[-1]
-    return x.numel() // cols, cols
 
 
 def _same(t, x, shape, what, dtype=None):
     if t.device != x.device:
         raise ValueError(f"nvfp4: {what} must be on {x.device}, not {t.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"nvfp4: {what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"nvfp4: {what} must be {dtype}, not {t.dtype}")
@@ -138,12 +146,27 @@ class Normed(NamedTuple):
     amax: "object"    # float32 [1] or None: max |y|, the amax of y's quantization
 
 
+def _rows(x):
+    """(rows, cols, type) of a norm's input."""
+    if _torch is None:
+        _load_torch()
+    shape = x.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError("layer_norm: x must have a last dimension of at least 1")
+    if not x.is_cuda:
+        raise ValueError("nvfp4: tensors must live on a CUDA device")
+    return x.numel() // shape[-1], shape[-1], _type_of(x, "x")
+
+
 def _affine(x, weight, bias, cols):
     """The type of weight and bias, which agree."""
-    given = [(t, name) for t, name in ((weight, "weight"), (bias, "bias")) if t is not None]
-    for t, name in given:
-        _same(t, x, (cols,), name, given[0][0].dtype)
-    return _type_of(*given[0]) if given else TYPE_F32
+    if weight is None and bias is None:
+        return TYPE_F32
+    first = bias if weight is None else weight
+    _same(first, x, (cols,), "bias" if weight is None else "weight")
+    if bias is not None and bias is not first:
+        _same(bias, x, (cols,), "bias", first.dtype)
+    return _type_of(first, "weight and bias")
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, with_stats=True, with_amax=False,
@@ -151,44 +174,52 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, with_stats=
     """Layer norm of BF16 or FP32 x over its last dimension; weight and bias (BF16 or FP32, [cols])
     may be None. ``with_stats`` returns what the backward pass needs, ``with_amax`` the amax of
     y, ready for ``quantize`` and ``quantize_for_gemm``. No autograd: see ``layer_norm``."""
-    import torch
-
-    rows, cols = _rows_cols(x, "layer_norm")
-    x_type, w_type = _type_of(x, "x"), _affine(x, weight, bias, cols)
-    with _on(x.device):
-        y = torch.empty_like(x)
-        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device) if with_stats else None
-        mean, rstd = (stats[0], stats[1]) if with_stats else (None, None)
-        top = torch.empty(1, dtype=torch.float32, device=x.device) if with_amax else None
-        nvfp4_layer_norm(x, x_type, weight, bias, w_type, rows, cols, eps, y, mean, rstd, top, stream)
-        _lend(stream, *(t for t in (y, stats, top) if t is not None))
+    rows, cols, x_type = _rows(x)
+    w_type = _affine(x, weight, bias, cols)
+    device = x.device
+    with _on(device):
+        source = _ptr(x)   # refuses what is not contiguous before anything is allocated
+        y = _torch.empty_like(x)
+        mean, rstd = _torch.empty((2, rows), dtype=_torch.float32, device=device).unbind() if with_stats else (None, None)
+        top = _torch.empty(1, dtype=_torch.float32, device=device) if with_amax else None
+        status = load().nvfp4_layer_norm(source, x_type, _ptr(weight), _ptr(bias), w_type, rows, cols, eps, y.data_ptr(),
+                                         _ptr(mean), _ptr(rstd), _ptr(top), _raw(stream, device))
+        if status:
+            _check(status, "nvfp4_layer_norm")
+        if stream is not None:
+            _lend(stream, y, mean, top)
     return Normed(y, mean, rstd, top)
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, with_weight=True, with_bias=True, stream=None):
     """(dx, dweight, dbias) of layer norm from its input and the statistics of its forward pass.
     dweight and dbias have the weight's type (FP32 without one); None where not asked for."""
-    import torch
-
-    rows, cols = _rows_cols(x, "layer_norm_backward")
+    rows, cols, x_type = _rows(x)
     _same(dy, x, x.shape, "dy", x.dtype)
-    _same(mean, x, (rows,), "mean", torch.float32)
-    _same(rstd, x, (rows,), "rstd", torch.float32)
-    x_type, w_type = _type_of(x, "x"), _affine(x, weight, None, cols)
-    with _on(x.device):
-        dx = torch.empty_like(x)
-        grads = [torch.empty(cols, dtype=torch.float32 if weight is None else weight.dtype, device=x.device) if asked
-                 else None for asked in (with_weight, with_bias)]
-        size = nvfp4_layer_norm_workspace(rows, cols) if with_weight or with_bias else 0
-        work = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
-        nvfp4_layer_norm_backward(dy, x, x_type, weight, w_type, mean, rstd, rows, cols, dx, *grads, work, size, stream)
-        _lend(stream, *(t for t in (dx, *grads, work) if t is not None))
-    return dx, grads[0], grads[1]
+    _same(mean, x, (rows,), "mean", _torch.float32)
+    _same(rstd, x, (rows,), "rstd", _torch.float32)
+    w_type = _affine(x, weight, None, cols)
+    device = x.device
+    with _on(device):
+        source = _ptr(x)
+        dx = _torch.empty_like(x)
+        dtype = _torch.float32 if weight is None else weight.dtype
+        dweight = _torch.empty(cols, dtype=dtype, device=device) if with_weight else None
+        dbias = _torch.empty(cols, dtype=dtype, device=device) if with_bias else None
+        size = load().nvfp4_layer_norm_workspace(rows, cols) if with_weight or with_bias else 0
+        work = _torch.empty(size, dtype=_torch.uint8, device=device) if size else None
+        status = load().nvfp4_layer_norm_backward(_ptr(dy), source, x_type, _ptr(weight), w_type, _ptr(mean), _ptr(rstd), rows, cols,
+                                                  dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(work), size, _raw(stream, device))
+        if status:
+            _check(status, "nvfp4_layer_norm_backward")
+        if stream is not None:
+            _lend(stream, dx, dweight, dbias, work)
+    return dx, dweight, dbias
 
 
 @functools.lru_cache(maxsize=None)
 def _layer_norm_function():
-    import torch
+    torch = _torch
 
     class _LayerNorm(torch.autograd.Function):
         @staticmethod
@@ -217,8 +248,7 @@ def _layer_norm_function():
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, with_amax=False):
     """y, or (y, amax): layer norm with autograd through x, weight and bias. The amax [1] is that
     of y's quantization (``fakequant_ste(y, amax_values=amax)``, ``quantize_for_gemm``)."""
-    import torch
-
+    torch = _torch or _load_torch()
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
         return _layer_norm_function().apply(x, weight, bias, eps, with_amax)
     r = layer_norm_forward(x, weight, bias, eps, False, with_amax)
@@ -233,8 +263,7 @@ class GradientList:
     must not overlap on the GPU."""
 
     def __init__(self, grads, device, records):
-        import torch
-
+        torch = _torch
         self.grads, self.device, self.count = grads, device, len(records)
         array = (OptTensor * max(1, len(records)))(*records)
         size = nvfp4_tensor_plan_bytes(array, len(records))
@@ -244,6 +273,7 @@ class GradientList:
         self.chunks = nvfp4_tensor_plan(array, len(records), image.data_ptr(), size)
         self.table = image.to(device)
         self.work = torch.zeros(_GRAD_NORM_WORKSPACE, dtype=torch.uint8, device=device)
+        self.table_ptr, self.work_ptr = self.table.data_ptr(), self.work.data_ptr()
 
 
 class AdamWPlan(GradientList):
@@ -275,8 +305,7 @@ class AdamWPlan(GradientList):
 
 def _control(steps, betas):
     """nvfp4_adamw_control after `steps` steps, as 8 words on the host."""
-    import torch
-
+    torch = _torch
     if not 0 <= steps < 1 << 32:
         raise ValueError("nvfp4: the number of steps must be in [0, 2^32)")
     powers = torch.tensor([betas[0] ** steps, betas[1] ** steps], dtype=torch.float64).view(torch.int32)
@@ -285,6 +314,8 @@ def _control(steps, betas):
 
 
 def _list_of(tensors, what):
+    if _torch is None:
+        _load_torch()
     tensors = list(tensors)
     if not tensors or not sum(t.numel() for t in tensors):
         raise ValueError(f"nvfp4: {what} are empty")
@@ -312,9 +343,8 @@ def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=
     FP32 master of every BF16 parameter; without one a BF16 parameter is rounded stochastically.
     ``weight_decay``: one number, or one for each tensor. ``seed`` (32 bits) of the stochastic
     rounding. ``step``: steps taken before. States start at zero, masters at the parameters."""
-    import torch
-
     params, grads = _list_of(params, "params"), _list_of(grads, "grads")
+    torch = _torch
     if len(params) != len(grads):
         raise ValueError("adamw_plan: one gradient for each parameter")
     decays = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
@@ -358,6 +388,7 @@ def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=
         plan.exp_avg_scale, plan.exp_avg_sq_scale = flat.get("exp_avg_scale"), flat.get("exp_avg_sq_scale")
         plan.control = _control(step, plan.betas).to(device)
         plan.amax = torch.zeros(len(params), dtype=torch.float32, device=device) if with_amax else None
+        plan.control_ptr, plan.amax_ptr = plan.control.data_ptr(), plan.amax.data_ptr() if with_amax else None
     return plan
 
 
@@ -365,29 +396,35 @@ def grad_norm(grads: GradientList, max_norm: float = math.inf, stream=None):
     """(norm, scale), each [1] on the device: the norm of all gradients of the list together and
     min(1, max_norm / (norm + 1e-6)). A norm that is not finite gives a NaN scale, with which
     ``adamw`` leaves everything as it is."""
-    import torch
-
-    with _on(grads.device):
-        out = torch.empty((2, 1), dtype=torch.float32, device=grads.device)
-        nvfp4_grad_norm(grads.table, grads.chunks, max_norm, out[0], out[1], grads.work, stream)
-        _lend(stream, out)
-    return out[0], out[1]
+    if not isinstance(grads, GradientList):
+        raise ValueError("grad_norm: needs a list of gradient_list, or a plan of adamw_plan")
+    device = grads.device
+    with _on(device):
+        norm, scale = _torch.empty((2, 1), dtype=_torch.float32, device=device).unbind()
+        status = load().nvfp4_grad_norm(grads.table_ptr, grads.chunks, max_norm, norm.data_ptr(), scale.data_ptr(), grads.work_ptr,
+                                        _raw(stream, device))
+        if status:
+            _check(status, "nvfp4_grad_norm")
+        if stream is not None:
+            _lend(stream, norm)
+    return norm, scale
 
 
 def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
     """One AdamW step, in place. ``lr``: a number, or an FP32 [1] tensor that the kernel reads (a
     captured call then follows it; the count of steps is kept on the device anyway). ``scale``:
     an FP32 [1] factor of the gradients, as ``grad_norm`` gives it."""
-    import torch
-
     if not isinstance(plan, AdamWPlan):
         raise ValueError("adamw: needs a plan of adamw_plan")
     lr_device = None
-    if isinstance(lr, torch.Tensor):
-        _same(lr, plan.control, (1,), "lr", torch.float32)
-        lr, lr_device = 0.0, lr
+    if isinstance(lr, _torch.Tensor):
+        _same(lr, plan.control, (1,), "lr", _torch.float32)
+        lr, lr_device = 0.0, lr.data_ptr()
     if scale is not None:
-        _same(scale, plan.control, (1,), "scale", torch.float32)
+        _same(scale, plan.control, (1,), "scale", _torch.float32)
+        scale = scale.data_ptr()
     with _on(plan.device):
-        nvfp4_adamw(plan.table, plan.chunks, plan.state_bits, plan.control, lr, lr_device, plan.betas[0], plan.betas[1], plan.eps, plan.seed,
-                    scale, plan.amax, plan.count if plan.amax is not None else 0, stream)
+        status = load().nvfp4_adamw(plan.table_ptr, plan.chunks, plan.state_bits, plan.control_ptr, lr, lr_device, plan.betas[0],
+                                    plan.betas[1], plan.eps, plan.seed, scale, plan.amax_ptr, plan.count, _raw(stream, plan.device))
+        if status:
+            _check(status, "nvfp4_adamw")
