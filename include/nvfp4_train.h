@@ -117,7 +117,7 @@ NVFP4_API nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64_
  *   norm  = sqrt(S over all tensors of g^2);  scale = min(1, max_norm / (norm + 1e-6))
  * scale is NaN when the norm is not finite: nvfp4_adamw then leaves everything as it is.
  *   plan       device copy of a nvfp4_tensor_plan image                             (in)
- *   chunks     as nvfp4_tensor_plan gave it
+ *   chunks     as nvfp4_tensor_plan gave it for this plan: the plan is read by it
  *   max_norm   >= 0, infinity allowed (scale = 1); else NVFP4_ERR_VALUE
  *   norm       [1] float                                                            (out)
  *   scale      [1] float                                                            (out)

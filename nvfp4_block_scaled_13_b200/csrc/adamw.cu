@@ -36,7 +36,9 @@ constexpr int kMaxParts = 2048;            // CTAs of the gradient norm
 
 enum Kind : uint32_t { kGradients = 1, kOptimizer32 = 2, kOptimizer8 = 3 };
 
-// The plan's image: Header, Tensor[count], Chunk[chunks]; every part a multiple of 16 bytes.
+// The plan's image: Header, Chunk[chunks], Tensor[count]; every part a multiple of 16 bytes. A kernel
+// is given the number of chunks, so that it can look at its first chunk, the header and the control
+// block at once: a short list's time is the chain of such reads.
 struct Header {
     uint32_t magic, kind;
     uint32_t count, chunks;
@@ -55,22 +57,29 @@ static_assert(sizeof(Header) == 32 && sizeof(nvfp4_opt_tensor) == 88 && sizeof(C
 // kVector: every pointer suits the step's whole accesses; kGradVector: the gradient the norm's.
 enum : uint32_t { kGradF32 = 1, kParamF32 = 2, kMaster = 4, kVector = 8, kGradVector = 16 };
 
+__host__ __device__ inline size_t tensor_offset(uint32_t chunks) {
+    return sizeof(Header) + (sizeof(Chunk) * size_t(chunks) + 15) / 16 * 16;
+}
+
 struct Image {
     const Header* header;
-    const Tensor* tensors;
     const Chunk* chunks;
-};
+    const Tensor* tensors;
 
-__host__ __device__ inline size_t tensor_offset() { return sizeof(Header); }
-__host__ __device__ inline size_t chunk_offset(uint32_t count) { return sizeof(Header) + sizeof(Tensor) * size_t(count); }
+    __device__ __forceinline__ Image(const void* plan, uint32_t count) {
+        const char* p = static_cast<const char*>(plan);
+        header = reinterpret_cast<const Header*>(p);
+        chunks = reinterpret_cast<const Chunk*>(p + sizeof(Header));
+        tensors = reinterpret_cast<const Tensor*>(p + tensor_offset(count));
+    }
+};
 
 // The chunks of a list, cut into equal ranges for the CTAs, as runs inside one tensor: a CTA streams
 // through a long piece of memory and looks at the tables rarely.
 struct Runs {
     uint32_t next, end;
 
-    __device__ __forceinline__ explicit Runs(const Image& image) {
-        const uint64_t chunks = image.header->chunks;
+    __device__ __forceinline__ explicit Runs(uint64_t chunks) {
         next = static_cast<uint32_t>(chunks * blockIdx.x / gridDim.x);
         end = static_cast<uint32_t>(chunks * (blockIdx.x + 1) / gridDim.x);
     }
@@ -82,13 +91,6 @@ struct Runs {
         next += static_cast<uint32_t>(run);
     }
 };
-
-__device__ __forceinline__ Image image_of(const void* plan) {
-    const char* p = static_cast<const char*>(plan);
-    const Header* h = reinterpret_cast<const Header*>(p);
-    return {h, reinterpret_cast<const Tensor*>(p + tensor_offset()),
-            reinterpret_cast<const Chunk*>(p + chunk_offset(h->count))};
-}
 
 // Eight elements from p[i]: one vector access, or the elements below n one by one.
 template <typename T>
@@ -228,6 +230,7 @@ __shared__ Tensor tensors[kThreads / 32];
 
 struct StepArgs {
     const void* plan;
+    uint32_t chunks;
     nvfp4_adamw_control* control;
     float lr;
     const float* lr_device;
@@ -722,8 +725,19 @@ __device__ __forceinline__ void publish_top(uint32_t& top, bool halves, uint32_t
 template <bool EIGHT>
 __global__ void __launch_bounds__(kThreads, kStepCtas<EIGHT>) adamw_kernel(const StepArgs a) {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Image image = image_of(a.plan);
-    if (image.header->magic != kMagic || image.header->kind != (EIGHT ? kOptimizer8 : kOptimizer32)) return;
+    const Image image(a.plan, a.chunks);
+    Runs runs(a.chunks);
+    Chunk chunk{};
+    // Each warp keeps the tensor's description in shared memory.
+    const auto describe = [&]() {
+        if (runs.next < runs.end) {
+            chunk = image.chunks[runs.next];
+            __syncwarp();
+            if (lane < sizeof(Tensor) / 4)
+                reinterpret_cast<uint32_t*>(&tensors[warp])[lane] = reinterpret_cast<const uint32_t*>(&image.tensors[chunk.tensor])[lane];
+            __syncwarp();
+        }
+    };
     if (threadIdx.x == 0) {
         Factors f;
         f.beta1 = static_cast<float>(a.beta1);
@@ -738,20 +752,17 @@ __global__ void __launch_bounds__(kThreads, kStepCtas<EIGHT>) adamw_kernel(const
         f.key = mix(a.seed + kGolden * a.control->step);
         factors = f;
     }
+    const Header header = *image.header;
+    describe();
     __syncthreads();
+    if (header.magic != kMagic || header.kind != (EIGHT ? kOptimizer8 : kOptimizer32) || header.chunks != a.chunks) return;
     const Factors& f = factors;
     const bool takes_place = isfinite(f.scale);
-    const int64_t length = image.header->chunk_elements;
+    const int64_t length = header.chunk_elements;
     uint32_t top = 0, last = 0xFFFFFFFFu;
     bool halves = false;
-    Runs runs(image);
-    while (runs.next < runs.end) {
-        const Chunk chunk = image.chunks[runs.next];
-        // each warp keeps the tensor's description in shared memory: registers are scarce below
-        __syncwarp();
-        if (lane < sizeof(Tensor) / 4)
-            reinterpret_cast<uint32_t*>(&tensors[warp])[lane] = reinterpret_cast<const uint32_t*>(&image.tensors[chunk.tensor])[lane];
-        __syncwarp();
+    for (bool described = true; runs.next < runs.end; described = false) {
+        if (!described) describe();
         const Tensor& t = tensors[warp];
         if (a.amax && last != 0xFFFFFFFFu && last != chunk.tensor) publish_top(top, halves, a.amax + last);
         last = chunk.tensor;
@@ -873,17 +884,20 @@ __device__ __forceinline__ double norm_run(const Tensor& t, int64_t lo, int64_t 
     return sum;
 }
 
-__global__ void __launch_bounds__(kThreads, kNormCtas) grad_norm_kernel(const void* plan, float max_norm, float* norm, float* scale,
+__global__ void __launch_bounds__(kThreads, kNormCtas) grad_norm_kernel(const void* plan, uint32_t chunks, float max_norm, float* norm, float* scale,
                                                              NormWorkspace* work) {
     __shared__ double shared[kThreads / 32];
     __shared__ bool is_last;
-    const Image image = image_of(plan);
-    if (image.header->magic != kMagic) return;
-    const int64_t length = image.header->chunk_elements;
+    const Image image(plan, chunks);
+    Runs runs(chunks);
+    Chunk chunk{};
+    if (runs.next < runs.end) chunk = image.chunks[runs.next];
+    const Header header = *image.header;
+    if (header.magic != kMagic || header.chunks != chunks) return;
+    const int64_t length = header.chunk_elements;
     double sum = 0.0;
-    Runs runs(image);
-    while (runs.next < runs.end) {
-        const Chunk chunk = image.chunks[runs.next];
+    for (bool first = true; runs.next < runs.end; first = false) {
+        if (!first) chunk = image.chunks[runs.next];
         const Tensor& t = image.tensors[chunk.tensor];
         int64_t lo, hi;
         runs.take(chunk, length, t.d.numel, lo, hi);
@@ -942,7 +956,7 @@ bool count_chunks(const nvfp4_opt_tensor* tensors, int64_t count, int64_t* lengt
 }
 
 int64_t plan_bytes(int64_t count, int64_t chunks) {
-    return static_cast<int64_t>(chunk_offset(static_cast<uint32_t>(count))) + (chunks * static_cast<int64_t>(sizeof(Chunk)) + 15) / 16 * 16;
+    return static_cast<int64_t>(tensor_offset(static_cast<uint32_t>(chunks)) + sizeof(Tensor) * static_cast<size_t>(count));
 }
 
 int64_t size_of(int32_t type) { return type == NVFP4_TYPE_F32 ? 4 : 2; }
@@ -1059,7 +1073,7 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
     header.chunks = static_cast<uint32_t>(chunks);
     header.chunk_elements = static_cast<uint32_t>(length);
     memcpy(out, &header, sizeof header);
-    char* next = out + chunk_offset(header.count);
+    char* next = out + sizeof(Header);
     for (int64_t i = 0; i < count; ++i) {
         Tensor t{};
         t.d = tensors[i];
@@ -1074,7 +1088,7 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
                 (state == 4 || (aligned_to(t.d.exp_avg_scale, 4) && aligned_to(t.d.exp_avg_sq_scale, 4))))
                 t.variant |= kVector;
         }
-        memcpy(out + tensor_offset() + sizeof(Tensor) * i, &t, sizeof t);
+        memcpy(out + tensor_offset(header.chunks) + sizeof(Tensor) * i, &t, sizeof t);
         for (int64_t c = 0; c * length < t.d.numel; ++c, next += sizeof(Chunk)) {
             const Chunk chunk{static_cast<uint32_t>(i), static_cast<uint32_t>(c)};
             memcpy(next, &chunk, sizeof chunk);
@@ -1087,12 +1101,12 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
 extern "C" nvfp4_status nvfp4_grad_norm(const void* plan, int64_t chunks, float max_norm, float* norm, float* scale,
                                         void* workspace, cudaStream_t stream) {
     if (plan == nullptr || norm == nullptr || scale == nullptr || workspace == nullptr) return NVFP4_ERR_NULL;
-    if (chunks < 0) return NVFP4_ERR_SHAPE;
+    if (chunks < 0 || chunks > 0xFFFFFFFFll) return NVFP4_ERR_SHAPE;
     if (!(max_norm >= 0.0f)) return NVFP4_ERR_VALUE;
     if (!aligned_to(plan, 16) || !aligned_to(norm, 4) || !aligned_to(scale, 4) || !aligned_to(workspace, 16))
         return NVFP4_ERR_ALIGN;
     const unsigned grid = std::min<unsigned>(resident_grid(chunks, kNormCtas), kMaxParts);
-    grad_norm_kernel<<<grid, kThreads, 0, stream>>>(plan, max_norm, norm, scale, static_cast<NormWorkspace*>(workspace));
+    grad_norm_kernel<<<grid, kThreads, 0, stream>>>(plan, static_cast<uint32_t>(chunks), max_norm, norm, scale, static_cast<NormWorkspace*>(workspace));
     return launched();
 }
 
@@ -1100,7 +1114,7 @@ extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t st
                                     const float* lr_device, double beta1, double beta2, float eps, uint32_t seed,
                                     const float* scale, float* amax, int64_t count, cudaStream_t stream) {
     if (plan == nullptr || control == nullptr) return NVFP4_ERR_NULL;
-    if (chunks < 0 || count < 0) return NVFP4_ERR_SHAPE;
+    if (chunks < 0 || chunks > 0xFFFFFFFFll || count < 0) return NVFP4_ERR_SHAPE;
     if ((state_bits != 32 && state_bits != 8) || (lr_device == nullptr && !(lr >= 0.0f && lr <= FLT_MAX)) || !(beta1 >= 0.0 && beta1 < 1.0) ||
         !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0f && eps <= FLT_MAX))
         return NVFP4_ERR_VALUE;
@@ -1109,7 +1123,7 @@ extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t st
         return NVFP4_ERR_ALIGN;
     if (amax && count > 0 && cudaMemsetAsync(amax, 0, static_cast<size_t>(count) * 4, stream) != cudaSuccess)
         return NVFP4_ERR_CUDA;
-    const StepArgs a{plan, control, lr, lr_device, beta1, beta2, eps, seed, scale, reinterpret_cast<uint32_t*>(amax)};
+    const StepArgs a{plan, static_cast<uint32_t>(chunks), control, lr, lr_device, beta1, beta2, eps, seed, scale, reinterpret_cast<uint32_t*>(amax)};
     if (state_bits == 32) {
         adamw_kernel<false><<<resident_grid(chunks, kStepCtas<false>), kThreads, 0, stream>>>(a);
     } else {

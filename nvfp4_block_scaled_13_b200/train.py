@@ -128,8 +128,14 @@ def _lend(stream, *tensors):
             t.record_stream(stream)
 
 
+def _address(t):
+    if not t.is_contiguous():
+        raise ValueError("nvfp4: tensors must be contiguous")
+    return t.data_ptr()
+
+
 def _same(t, x, shape, what, dtype=None):
-    if t.device != x.device:
+    if t.get_device() != x.get_device():
         raise ValueError(f"nvfp4: {what} must be on {x.device}, not {t.device}")
     if t.shape != shape:
         raise ValueError(f"nvfp4: {what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -176,18 +182,23 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, with_stats=
     y, ready for ``quantize`` and ``quantize_for_gemm``. No autograd: see ``layer_norm``."""
     rows, cols, x_type = _rows(x)
     w_type = _affine(x, weight, bias, cols)
-    device = x.device
+    device, mean, rstd, top = x.device, None, None, None
     with _on(device):
-        source = _ptr(x)   # refuses what is not contiguous before anything is allocated
+        source = _address(x)   # refuses what is not contiguous before anything is allocated
+        w, b = None if weight is None else _address(weight), None if bias is None else _address(bias)
         y = _torch.empty_like(x)
-        mean, rstd = _torch.empty((2, rows), dtype=_torch.float32, device=device).unbind() if with_stats else (None, None)
-        top = _torch.empty(1, dtype=_torch.float32, device=device) if with_amax else None
-        status = load().nvfp4_layer_norm(source, x_type, _ptr(weight), _ptr(bias), w_type, rows, cols, eps, y.data_ptr(),
-                                         _ptr(mean), _ptr(rstd), _ptr(top), _raw(stream, device))
+        if with_stats:
+            mean = _torch.empty(rows, dtype=_torch.float32, device=device)
+            rstd = _torch.empty(rows, dtype=_torch.float32, device=device)
+        if with_amax:
+            top = _torch.empty(1, dtype=_torch.float32, device=device)
+        status = load().nvfp4_layer_norm(source, x_type, w, b, w_type, rows, cols, eps, y.data_ptr(),
+                                         mean.data_ptr() if with_stats else None, rstd.data_ptr() if with_stats else None,
+                                         top.data_ptr() if with_amax else None, _raw(stream, device))
         if status:
             _check(status, "nvfp4_layer_norm")
         if stream is not None:
-            _lend(stream, y, mean, top)
+            _lend(stream, y, mean, rstd, top)
     return Normed(y, mean, rstd, top)
 
 
@@ -199,17 +210,22 @@ def layer_norm_backward(dy, x, weight, mean, rstd, with_weight=True, with_bias=T
     _same(mean, x, (rows,), "mean", _torch.float32)
     _same(rstd, x, (rows,), "rstd", _torch.float32)
     w_type = _affine(x, weight, None, cols)
-    device = x.device
+    device, dweight, dbias, work, size = x.device, None, None, None, 0
     with _on(device):
-        source = _ptr(x)
+        sources = _address(dy), _address(x)
+        w = None if weight is None else _address(weight)
         dx = _torch.empty_like(x)
         dtype = _torch.float32 if weight is None else weight.dtype
-        dweight = _torch.empty(cols, dtype=dtype, device=device) if with_weight else None
-        dbias = _torch.empty(cols, dtype=dtype, device=device) if with_bias else None
-        size = load().nvfp4_layer_norm_workspace(rows, cols) if with_weight or with_bias else 0
-        work = _torch.empty(size, dtype=_torch.uint8, device=device) if size else None
-        status = load().nvfp4_layer_norm_backward(_ptr(dy), source, x_type, _ptr(weight), w_type, _ptr(mean), _ptr(rstd), rows, cols,
-                                                  dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(work), size, _raw(stream, device))
+        if with_weight:
+            dweight = _torch.empty(cols, dtype=dtype, device=device)
+        if with_bias:
+            dbias = _torch.empty(cols, dtype=dtype, device=device)
+        if with_weight or with_bias:
+            size = load().nvfp4_layer_norm_workspace(rows, cols)
+            work = _torch.empty(size, dtype=_torch.uint8, device=device)
+        status = load().nvfp4_layer_norm_backward(*sources, x_type, w, w_type, _address(mean), _address(rstd), rows, cols, dx.data_ptr(),
+                                                  dweight.data_ptr() if with_weight else None, dbias.data_ptr() if with_bias else None,
+                                                  work.data_ptr() if size else None, size, _raw(stream, device))
         if status:
             _check(status, "nvfp4_layer_norm_backward")
         if stream is not None:
@@ -400,13 +416,14 @@ def grad_norm(grads: GradientList, max_norm: float = math.inf, stream=None):
         raise ValueError("grad_norm: needs a list of gradient_list, or a plan of adamw_plan")
     device = grads.device
     with _on(device):
-        norm, scale = _torch.empty((2, 1), dtype=_torch.float32, device=device).unbind()
+        norm = _torch.empty(1, dtype=_torch.float32, device=device)
+        scale = _torch.empty(1, dtype=_torch.float32, device=device)
         status = load().nvfp4_grad_norm(grads.table_ptr, grads.chunks, max_norm, norm.data_ptr(), scale.data_ptr(), grads.work_ptr,
                                         _raw(stream, device))
         if status:
             _check(status, "nvfp4_grad_norm")
         if stream is not None:
-            _lend(stream, norm)
+            _lend(stream, norm, scale)
     return norm, scale
 
 

@@ -140,7 +140,8 @@ def test_plan_covers_every_element_once(lengths):
     magic, kind, count, n_chunks, length = struct.unpack_from("<5I", image)
     assert kind == 2 and count == len(lengths) and n_chunks == chunks and length % 2048 == 0
     covered = [0] * count
-    at = 32 + count * 104
+    at = 32
+    assert len(image) == 32 + (8 * chunks + 15) // 16 * 16 + count * 104
     for c in range(chunks):
         t, index = struct.unpack_from("<2I", image, at + 8 * c)
         assert index * length == covered[t], "a tensor's chunks come in order"
