@@ -45,6 +45,7 @@ struct NormArgs {
     float* mean;
     float* rstd;
     uint32_t* amax;
+    int row_threads;   // of norm_group_kernel where a row has a CTA or a cluster
 };
 
 struct NormGradArgs {
@@ -59,6 +60,7 @@ struct NormGradArgs {
     void* dx;
     float* sums;   // [2][parts][cols]: partial dweight, partial dbias; or NULL
     int parts;
+    int row_threads;
 };
 
 // ---- units ---------------------------------------------------------------------------------
@@ -230,8 +232,8 @@ __device__ __forceinline__ float lane_sum(float v) {
     return v;
 }
 
-// LANES of a row that a CTA has, or a cluster of CTAs.
-constexpr int kCta = 0, kCluster = -1;
+// LANES of a row that has a CTA, a cluster of CTAs, or some warps of a CTA (`row_threads`).
+constexpr int kCta = 0, kCluster = -1, kRows = -2;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -247,47 +249,59 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+template <int LANES>
+__device__ __forceinline__ void sync_all() {
+    if (LANES == kCluster) {
+        cluster_sync();
+    } else {
+        __syncthreads();
+    }
+}
+
 // Partial sums of the warps of a row, in two sets that alternate: the barrier of the next
 // reduction separates this one's reads from the writes after next, so a reduction has one
-// barrier. In a cluster every warp leaves its sum in the shared memory of every CTA.
+// barrier. In a cluster every warp leaves its sum in the shared memory of every CTA; row groups
+// inside a CTA (kRows, of at most four warps) have 16 places and a barrier each.
 template <int LANES>
 struct WarpSums {
-    static constexpr int kFours = LANES == kCluster ? 32 : 4;   // 8 CTAs of 16 warps, or 16 warps
+    static constexpr int kFours = LANES == kCta ? 4 : 32;   // 16 warps; 8 CTAs of 16 warps, or 8 groups of 16 places
     float4 set[2][kFours];
 
     __device__ __forceinline__ void clear() {
         for (int k = threadIdx.x; k < 2 * kFours; k += blockDim.x) (&set[0][0])[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    __device__ __forceinline__ void put(int which, float v) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __device__ __forceinline__ void put(int which, int group, int t, float v) {
         float* to = reinterpret_cast<float*>(set[which]);
+        const int lane = threadIdx.x & 31;
         if (LANES == kCluster) {
             if (lane < static_cast<int>(cluster_size())) {
-                const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to + cluster_rank() * (blockDim.x >> 5) + warp));
+                const uint32_t at =
+                    static_cast<uint32_t>(__cvta_generic_to_shared(to + cluster_rank() * (blockDim.x >> 5) + (threadIdx.x >> 5)));
                 uint32_t remote;
                 asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(lane));
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
             }
         } else if (lane == 0) {
-            to[warp] = v;
+            to[LANES == kRows ? group * 16 + (t >> 5) : threadIdx.x >> 5] = v;
         }
     }
-    __device__ __forceinline__ void sync() const {
-        if (LANES == kCluster) {
-            cluster_sync();
+    static __device__ __forceinline__ void sync(int group, int row_threads) {
+        if (LANES == kRows) {
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(row_threads) : "memory");
         } else {
-            __syncthreads();
+            sync_all<LANES>();
         }
     }
     __device__ __forceinline__ float four(int which, int k) const {
         const float4 p = set[which][k];
         return (p.x + p.y) + (p.z + p.w);
     }
-    __device__ __forceinline__ float total(int which) const {
+    __device__ __forceinline__ float total(int which, int group, int row_threads) const {
         if (LANES == kCluster) return warp_sum(four(which, threadIdx.x & 31));
+        if (LANES == kRows) return four(which, group * 4);   // at most four warps
         float s = four(which, 0);
         if (blockDim.x > 128) s += four(which, 1);
-        if (blockDim.x > 256) s += four(which, 2 % kFours) + four(which, 3 % kFours);
+        if (blockDim.x > 256) s += four(which, 2) + four(which, 3);
         return s;
     }
 };
@@ -319,7 +333,9 @@ __device__ __forceinline__ void publish_amax(uint32_t top, uint32_t* amax) {
 
 // ---- forward -------------------------------------------------------------------------------
 
-constexpr int kForwardStages = 4, kBackwardStages = 3;   // rows in the ring
+constexpr int kForwardStages = 4;   // rows in the ring
+// Backward: three (four and six were no faster).
+constexpr int kBackwardStages = 3;
 
 // Registers of a thread, and with them the CTAs that an SM holds (each of its four quarters has
 // 16384 registers).
@@ -329,7 +345,8 @@ constexpr int resident(int registers, int threads) {
     return std::max(1, std::min(32, 16384 / (registers * 32) * 4 / (threads / 32)));
 }
 
-// Which rows a thread's group takes, and the shift that they share.
+// Which rows a thread's group takes: the groups of a CTA take every ctas-th row in turn, which gives
+// all of them one shift.
 template <typename T, int LANES, bool SHIFTED>
 struct Group {
     int lanes, t, groups, index;
@@ -338,13 +355,14 @@ struct Group {
     int shift;
     int part;          // index of the CTA, or cluster, and of its partial row
 
-    __device__ __forceinline__ Group(const void* x, int64_t all_rows, int cols) {
+    __device__ __forceinline__ Group(const void* x, int64_t all_rows, int cols, int row_threads) {
         constexpr unsigned L = LANES > 0 ? LANES : 1;
         int64_t base = blockIdx.x, ctas = gridDim.x;
-        lanes = LANES > 0 ? LANES : static_cast<int>(blockDim.x);
-        t = static_cast<int>(LANES > 0 ? threadIdx.x % L : threadIdx.x);
-        groups = LANES > 0 ? static_cast<int>(blockDim.x / L) : 1;
-        index = LANES > 0 ? static_cast<int>(threadIdx.x / L) : 0;
+        const unsigned l = LANES > 0 ? L : LANES == kRows ? row_threads : blockDim.x;
+        lanes = static_cast<int>(l);
+        index = LANES > 0 || LANES == kRows ? static_cast<int>(threadIdx.x / l) : 0;
+        groups = LANES > 0 || LANES == kRows ? static_cast<int>(blockDim.x / l) : 1;
+        t = static_cast<int>(threadIdx.x) - index * lanes;
         if (LANES == kCluster) {
             const int size = static_cast<int>(cluster_size());
             t += static_cast<int>(cluster_rank() * blockDim.x);
@@ -353,8 +371,7 @@ struct Group {
             ctas /= size;
         }
         part = static_cast<int>(base);
-        base *= groups;
-        first = base + index;
+        first = base + index * ctas;
         step = ctas * groups;
         turns = static_cast<int>((all_rows - base + step - 1) / step);
         rows = first < all_rows ? static_cast<int>((all_rows - first + step - 1) / step) : 0;
@@ -369,7 +386,7 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
     constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
     extern __shared__ uint4 ring[];   // [S][Q][threads]
     __shared__ WarpSums<LANES> warp_sums;
-    const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols);
+    const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols, a.row_threads);
     const Columns<T, Q, SHIFTED> at(group.t, group.lanes, group.shift, a.cols);
     uint32_t mask[Q];
 #pragma unroll
@@ -399,7 +416,7 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
     }
     if (LANES <= 0) {
         warp_sums.clear();
-        warp_sums.sync();
+        sync_all<LANES>();
     }
     const float inv = 1.0f / static_cast<float>(a.cols), eps = a.eps;
     char* y = static_cast<char*>(a.y) + (group.first * a.cols + at.start(0)) * int64_t(sizeof(T));
@@ -424,9 +441,9 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
         sum2[0] = add2(sum2[0], sum2[1]);
         float sum = lane_sum<LANES>(sum2[0].x + sum2[0].y);
         if (LANES <= 0) {
-            warp_sums.put(0, sum);
-            warp_sums.sync();
-            sum = warp_sums.total(0);
+            warp_sums.put(0, group.index, group.t, sum);
+            warp_sums.sync(group.index, a.row_threads);
+            sum = warp_sums.total(0, group.index, a.row_threads);
         }
         const float mean = sum * inv;
         float2 square2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -441,9 +458,9 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
         square2[0] = add2(square2[0], square2[1]);
         float square = lane_sum<LANES>(square2[0].x + square2[0].y);
         if (LANES <= 0) {
-            warp_sums.put(1, square);
-            warp_sums.sync();
-            square = warp_sums.total(1);
+            warp_sums.put(1, group.index, group.t, square);
+            warp_sums.sync(group.index, a.row_threads);
+            square = warp_sums.total(1, group.index, a.row_threads);
         }
         const float rstd = rsqrtf(fmaf(square, inv, eps));
         if (LANES <= 0 || turn < group.rows) {
@@ -660,28 +677,45 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
 
 // ---- backward ------------------------------------------------------------------------------
 
-// Adds the column sums of the groups of a CTA in their order and writes the CTA's partial row.
-template <typename T, int Q, bool SHIFTED>
-__device__ __forceinline__ void join_groups(const float2 (&s)[Q][kUnit<T> / 2], const Columns<T, Q, SHIFTED>& at, int group,
-                                            int groups, float* shared, float* out) {
+// Adds the column sums of the row groups of a CTA, first those of a warp, and writes the CTA's
+// partial row. `shared`: [warps][cols].
+template <typename T, int Q, int LANES, bool SHIFTED>
+__device__ __forceinline__ void join_groups(float2 (&s)[Q][kUnit<T> / 2], const Columns<T, Q, SHIFTED>& at, float* shared, float* out) {
     constexpr int E = kUnit<T>;
-    for (int g = 0; g < groups; ++g) {
-        if (group == g) {
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();   // nobody uses the shared memory any more
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const uint32_t mask = at.mask(q);
+    for (int q = 0; q < Q; ++q) {
+        const uint32_t mask = at.mask(q);
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float v = j & 1 ? s[q][j / 2].y : s[q][j / 2].x;
-                    float* sum = shared + at.start(q) + j;
-                    if (mask >> j & 1u) *sum = g == 0 ? v : *sum + v;
-                }
-            }
+        for (int j = 0; j < E; ++j) {
+            float v = j & 1 ? s[q][j / 2].y : s[q][j / 2].x;
+#pragma unroll
+            for (int off = LANES; off < 32; off *= 2) v += __shfl_xor_sync(kFull, v, off);
+            if (lane < LANES && (mask >> j & 1u)) shared[(threadIdx.x >> 5) * at.cols + at.start(q) + j] = v;
         }
-        __syncthreads();
     }
-    for (int c = threadIdx.x; c < at.cols; c += blockDim.x) out[c] = shared[c];
     __syncthreads();
+    for (int c = threadIdx.x; c < at.cols; c += blockDim.x) {
+        float v = shared[c];
+        for (int w = 1; w < warps; ++w) v += shared[w * at.cols + c];
+        out[c] = v;
+    }
+}
+
+// Adds the sums of a CTA's row groups, thread by thread (a thread of each has the same columns), to
+// those of the first group.
+template <int PAIRS, typename Rows>
+__device__ __forceinline__ void join_rows(float2* s, const Rows& group, float2* shared) {
+    __syncthreads();   // nobody uses the shared memory any more
+    if (group.index > 0)
+#pragma unroll
+        for (int k = 0; k < PAIRS; ++k) shared[k * blockDim.x + threadIdx.x] = s[k];
+    __syncthreads();
+    if (group.index == 0)
+        for (int g = 1; g < group.groups; ++g)
+#pragma unroll
+            for (int k = 0; k < PAIRS; ++k) s[k] = add2(s[k], shared[k * blockDim.x + g * group.lanes + threadIdx.x]);
 }
 
 // A unit's column sums; `vector` where the partial rows lie as the operands' rows do.
@@ -702,13 +736,12 @@ __device__ __forceinline__ void store_sums(float* to, const float2 (&s)[E / 2], 
 
 template <typename T, int N, int LANES, bool SHIFTED>
 __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
-    constexpr int E = kUnit<T>, Q = N / E, H = E / 2, S = kBackwardStages;
+    constexpr int E = kUnit<T>, Q = N / E, H = E / 2, P = E / 4, S = kBackwardStages;
     constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
-    extern __shared__ uint4 ring[];   // [S][Q][x, dy][threads]
+    extern __shared__ uint4 ring[];   // [S][Q][x, dy][threads], then the weight [P][Q][lanes of the CTA's rows]
     let_next_start();
     __shared__ WarpSums<LANES> sums1, sums2;
-    __shared__ float joined[LANES > 0 ? LANES * N : 1];
-    const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols);
+    const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols, a.row_threads);
     const Columns<T, Q, SHIFTED> at(group.t, group.lanes, group.shift, a.cols);
     uint32_t mask[Q];
 #pragma unroll
@@ -734,18 +767,30 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
     };
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) fetch(slots + s * Q * 2 * slot_bytes);
-    float2 w[Q][H], sw[Q][H], sb[Q][H];
+    // The weight waits in registers; beside groups of lanes, of which a CTA has many, in shared memory.
+    float4* const weights = reinterpret_cast<float4*>(ring + S * Q * 2 * blockDim.x) + group.t;
+    float2 held[LANES > 0 ? 1 : Q][H], sw[Q][H], sb[Q][H];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), mask[q], 1.0f, w[q]);
+        if constexpr (LANES > 0) {
+            if (group.index == 0) {
+                float2 w[H];
+                load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), mask[q], 1.0f, w);
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    weights[(p * Q + q) * LANES] = make_float4(w[2 * p].x, w[2 * p].y, w[2 * p + 1].x, w[2 * p + 1].y);
+            }
+        } else {
+            load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), mask[q], 1.0f, held[q]);
+        }
 #pragma unroll
         for (int k = 0; k < H; ++k) sw[q][k] = sb[q][k] = make_float2(0.0f, 0.0f);
     }
     if (LANES <= 0) {
         sums1.clear();
         sums2.clear();
-        sums1.sync();
     }
+    sync_all<LANES>();
     const float inv = 1.0f / static_cast<float>(a.cols);
     char* dx = static_cast<char*>(a.dx) + (group.first * a.cols + at.start(0)) * int64_t(sizeof(T));
     const float *means = a.mean + group.first, *rstds = a.rstd + group.first;
@@ -755,7 +800,8 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
         next_rstd = *rstds;
     }
     uint32_t slot = slots, refill = slots + (S - 1) * Q * 2 * slot_bytes;
-    for (int turn = 0; turn < group.turns; ++turn) {
+    const int turns = LANES > 0 ? group.turns : group.rows;   // a warp's lanes make the same turns
+    for (int turn = 0; turn < turns; ++turn) {
         const float mean = next_mean, rstd = next_rstd;
         const bool exists = LANES <= 0 || turn < group.rows;   // a group past its last row adds nothing
         wait_copies<S - 2>();
@@ -775,7 +821,12 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
             for (int k = 0; k < H; ++k) {
                 sw[q][k] = fma2(h[q][k], xh[q][k], sw[q][k]);
                 sb[q][k] = add2(sb[q][k], h[q][k]);
-                h[q][k] = mul2(h[q][k], w[q][k]);
+                if constexpr (LANES > 0) {
+                    const float4 w = weights[(k / 2 * Q + q) * LANES];
+                    h[q][k] = mul2(h[q][k], k & 1 ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
+                } else {
+                    h[q][k] = mul2(h[q][k], held[q][k]);
+                }
                 s1 = add2(s1, h[q][k]);
                 s2 = fma2(h[q][k], xh[q][k], s2);
             }
@@ -792,11 +843,11 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
         }
         float t1 = lane_sum<LANES>(s1.x + s1.y), t2 = lane_sum<LANES>(s2.x + s2.y);
         if (LANES <= 0) {
-            sums1.put(turn & 1, t1);
-            sums2.put(turn & 1, t2);
-            sums1.sync();
-            t1 = sums1.total(turn & 1);
-            t2 = sums2.total(turn & 1);
+            sums1.put(turn & 1, group.index, group.t, t1);
+            sums2.put(turn & 1, group.index, group.t, t2);
+            sums1.sync(group.index, a.row_threads);
+            t1 = sums1.total(turn & 1, group.index, a.row_threads);
+            t2 = sums2.total(turn & 1, group.index, a.row_threads);
         }
         t1 *= -inv;
         t2 *= -inv;
@@ -816,13 +867,19 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
         float* out = a.sums + int64_t(group.part) * a.cols;
         float* out_b = out + int64_t(a.parts) * a.cols;
         if (LANES > 0) {
-            join_groups<T, Q, SHIFTED>(sw, at, group.index, group.groups, joined, out);
-            join_groups<T, Q, SHIFTED>(sb, at, group.index, group.groups, joined, out_b);
+            join_groups<T, Q, LANES, SHIFTED>(sw, at, reinterpret_cast<float*>(ring), out);
+            join_groups<T, Q, LANES, SHIFTED>(sb, at, reinterpret_cast<float*>(ring), out_b);
         } else {
+            if (LANES == kRows) {   // onto the first group's, in the groups' order
+                join_rows<Q * H>(&sw[0][0], group, reinterpret_cast<float2*>(ring));
+                join_rows<Q * H>(&sb[0][0], group, reinterpret_cast<float2*>(ring));
+            }
+            if (group.index == 0) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                store_sums<E>(out + at.start(q), sw[q], mask[q], !SHIFTED);
-                store_sums<E>(out_b + at.start(q), sb[q], mask[q], !SHIFTED);
+                for (int q = 0; q < Q; ++q) {
+                    store_sums<E>(out + at.start(q), sw[q], mask[q], !SHIFTED);
+                    store_sums<E>(out_b + at.start(q), sb[q], mask[q], !SHIFTED);
+                }
             }
         }
     }
@@ -926,38 +983,41 @@ nvfp4_status launched() { return cudaGetLastError() == cudaSuccess ? NVFP4_OK : 
 // How rows are given to threads.
 struct Cut {
     int elements;   // of a thread; 0: by norm_long_kernel and its like
-    int lanes;      // of a row: 8, 16, 32, kCta or kCluster
+    int lanes;      // of a row: 8, 16, 32, kCta, kRows or kCluster
     int threads;    // of a CTA
+    int row_threads;   // of those, a row's
     int cluster;    // CTAs of a row
     bool shifted;
 };
 
 // Rows that start on 16 bytes take whole units; others, where all operands' rows start at the same
 // place within 16 bytes, are shifted.
-Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent) {
+Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent, bool backward) {
     const int unit = 16 / size;
     const bool shifted = !aligned || cols % unit != 0;
     const int64_t need = cols + (shifted ? unit - 1 : 0);
-    if (!congruent) return {0, 0, 0, 1, false};
-    if (need <= 64) return {8, 8, 128, 1, shifted};
-    if (need <= 128) return {8, 16, 128, 1, shifted};
-    if (need <= 256) return {8, 32, 128, 1, shifted};
-    if (need <= 512) return {16, 32, 128, 1, shifted};
+    if (!congruent) return {0, 0, 0, 1, 1, false};
+    // backward one CTA an SM, so that few partial rows are left
+    const int threads = backward ? 512 : 128;
+    if (need <= 64) return {8, 8, threads, 8, 1, shifted};
+    if (need <= 128) return {8, 16, threads, 16, 1, shifted};
+    if (need <= 256) return {8, 32, threads, 32, 1, shifted};
+    if (need <= 512) return {16, 32, threads, 32, 1, shifted};
     for (int cluster = 1; cluster <= 8; cluster *= 2) {
-        const int64_t threads = (need + 512 * cluster - 1) / (512 * cluster) * 32;
-        if (threads <= 512) return {16, cluster == 1 ? kCta : kCluster, static_cast<int>(threads), cluster, shifted};
+        const int64_t row = (need + 512 * cluster - 1) / (512 * cluster) * 32;   // 16 elements a thread
+        if (row <= 512) {
+            const int groups = backward && row <= 128 ? static_cast<int>(512 / row) : 1;
+            return {16, cluster > 1 ? kCluster : groups > 1 ? kRows : kCta, static_cast<int>(row) * groups, static_cast<int>(row), cluster, shifted};
+        }
     }
-    return {0, 0, 0, 1, false};
+    return {0, 0, 0, 1, 1, false};
 }
 
 // Groups of CTAs (one, or a cluster) that share the rows: at most the `resident` ones, and so many
-// that every row group keeps its shift.
+// that all rows of one keep their shift: a multiple of `unit`, unless each has one row only.
 int64_t parts_of(const Cut& cut, int64_t rows, int64_t resident_ctas, int size) {
-    const int64_t groups = cut.lanes > 0 ? cut.threads / cut.lanes : 1, need = (rows + groups - 1) / groups;
-    const int64_t room = std::max<int64_t>(1, resident_ctas / cut.cluster);
-    if (need <= room) return need;
-    const int64_t unit = 16 / size;
-    return room * groups % unit == 0 ? room : std::max<int64_t>(unit, room / unit * unit);
+    const int64_t room = std::max<int64_t>(1, resident_ctas / cut.cluster), unit = 16 / size;
+    return rows <= room ? rows : std::max<int64_t>(unit, room / unit * unit);
 }
 
 // Partial rows of the backward pass.
@@ -1099,7 +1159,7 @@ nvfp4_status run_norm(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
 template <typename T, int N, int LANES, bool SHIFTED>
 nvfp4_status launch_grad(const NormGradArgs& a, const Cut& cut, cudaStream_t stream) {
     constexpr auto kernel = norm_grad_kernel<T, N, LANES, SHIFTED>;
-    const size_t smem = size_t(kBackwardStages) * 2 * N * sizeof(T) * cut.threads;
+    const size_t smem = size_t(kBackwardStages) * 2 * N * sizeof(T) * cut.threads + (LANES > 0 ? size_t(4) * N * LANES : 0);
     if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
     return launch<NormGradArgs>(kernel, dim3(static_cast<unsigned>(a.parts * cut.cluster)), cut.threads, cut.cluster, smem,
                                       false, stream, a);
@@ -1113,6 +1173,7 @@ nvfp4_status dispatch_grad(const NormGradArgs& a, const Cut& cut, cudaStream_t s
         case 32:
             return cut.elements == 8 ? launch_grad<T, 8, 32, SHIFTED>(a, cut, stream) : launch_grad<T, 16, 32, SHIFTED>(a, cut, stream);
         case kCta: return launch_grad<T, 16, kCta, SHIFTED>(a, cut, stream);
+        case kRows: return launch_grad<T, 16, kRows, SHIFTED>(a, cut, stream);
         default: return launch_grad<T, 16, kCluster, SHIFTED>(a, cut, stream);
     }
 }
@@ -1147,10 +1208,10 @@ extern "C" nvfp4_status nvfp4_layer_norm(const void* x, nvfp4_type x_type, const
         if (amax && cudaMemsetAsync(amax, 0, 4, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
         return NVFP4_OK;
     }
-    const Cut cut = cut_rows(cols, type_size(x_type), place(x) == 0, place(x) == place(y));
+    const Cut cut = cut_rows(cols, type_size(x_type), place(x) == 0, place(x) == place(y), false);
     const bool vector = !cut.shifted && place(weight) == 0 && place(bias) == 0;
     const NormArgs a{x, weight, bias, w_type == NVFP4_TYPE_F32, vector, rows, static_cast<int>(cols), eps, y, mean, rstd,
-                     reinterpret_cast<uint32_t*>(amax)};
+                     reinterpret_cast<uint32_t*>(amax), cut.row_threads};
     return x_type == NVFP4_TYPE_F32 ? run_norm<float>(a, cut, stream) : run_norm<bf16>(a, cut, stream);
 }
 
@@ -1161,7 +1222,7 @@ extern "C" int64_t nvfp4_layer_norm_workspace(int64_t rows, int64_t cols) {
     for (const int size : {2, 4})
         for (const bool aligned : {true, false})
             for (const bool congruent : {true, false})
-                parts = std::max(parts, backward_parts(cut_rows(cols, size, aligned, congruent), rows, cols, size));
+                parts = std::max(parts, backward_parts(cut_rows(cols, size, aligned, congruent, true), rows, cols, size));
     return 2 * parts * cols * 4;
 }
 
@@ -1189,10 +1250,10 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, const void* x,
     }
     if (sums && workspace_bytes < nvfp4_layer_norm_workspace(rows, cols)) return NVFP4_ERR_SHAPE;
     const int size = type_size(x_type);
-    const Cut cut = cut_rows(cols, size, place(x) == 0, place(x) == place(dy) && place(x) == place(dx));
+    const Cut cut = cut_rows(cols, size, place(x) == 0, place(x) == place(dy) && place(x) == place(dx), true);
     const bool vector = !cut.shifted && place(weight) == 0;
     const NormGradArgs a{dy, x, weight, w_type == NVFP4_TYPE_F32, vector, mean, rstd, rows, static_cast<int>(cols), dx,
-                         sums ? static_cast<float*>(workspace) : nullptr, static_cast<int>(backward_parts(cut, rows, cols, size))};
+                         sums ? static_cast<float*>(workspace) : nullptr, static_cast<int>(backward_parts(cut, rows, cols, size)), cut.row_threads};
     const nvfp4_status st = x_type == NVFP4_TYPE_F32 ? run_grad<float>(a, cut, stream) : run_grad<bf16>(a, cut, stream);
     if (st != NVFP4_OK || !sums) return st;
     const dim3 grid(static_cast<unsigned>((cols + 31) / 32), 2);
