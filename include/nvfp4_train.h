@@ -174,7 +174,8 @@ typedef struct {
  *              does not take place: only amax is written                             (in)
  *   amax       NULL, or [count] float: max |param| of each tensor as stored, the amax of its next
  *              fake-quantization; zero-filled first in stream order; 0 for an empty tensor (out)
- *   count      number of tensors of the plan, for amax
+ *   count      number of tensors of the plan, read where amax is given (another number: nothing is
+ *              done)
  * Calls on one control block or one list must not overlap on the GPU. One kernel. */
 NVFP4_API nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t state_bits,
                                    nvfp4_adamw_control* control, float lr, const float* lr_device, double beta1, double beta2, float eps, uint32_t seed,

@@ -239,6 +239,7 @@ struct StepArgs {
     uint32_t seed;
     const float* scale;
     uint32_t* amax;
+    uint32_t count;
 };
 
 // Root and reciprocal beside 8-bit states, whose step is bound by the instructions: the hardware's
@@ -755,7 +756,9 @@ __global__ void __launch_bounds__(kThreads, kStepCtas<EIGHT>) adamw_kernel(const
     const Header header = *image.header;
     describe();
     __syncthreads();
-    if (header.magic != kMagic || header.kind != (EIGHT ? kOptimizer8 : kOptimizer32) || header.chunks != a.chunks) return;
+    if (header.magic != kMagic || header.kind != (EIGHT ? kOptimizer8 : kOptimizer32) || header.chunks != a.chunks ||
+        (a.amax && header.count != a.count))
+        return;
     const Factors& f = factors;
     const bool takes_place = isfinite(f.scale);
     const int64_t length = header.chunk_elements;
@@ -1123,7 +1126,7 @@ extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t st
         return NVFP4_ERR_ALIGN;
     if (amax && count > 0 && cudaMemsetAsync(amax, 0, static_cast<size_t>(count) * 4, stream) != cudaSuccess)
         return NVFP4_ERR_CUDA;
-    const StepArgs a{plan, static_cast<uint32_t>(chunks), control, lr, lr_device, beta1, beta2, eps, seed, scale, reinterpret_cast<uint32_t*>(amax)};
+    const StepArgs a{plan, static_cast<uint32_t>(chunks), control, lr, lr_device, beta1, beta2, eps, seed, scale, reinterpret_cast<uint32_t*>(amax), static_cast<uint32_t>(count)};
     if (state_bits == 32) {
         adamw_kernel<false><<<resident_grid(chunks, kStepCtas<false>), kThreads, 0, stream>>>(a);
     } else {

@@ -441,7 +441,7 @@ def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
         _same(scale, plan.control, (1,), "scale", _torch.float32)
         scale = scale.data_ptr()
     with _on(plan.device):
-        status = load().nvfp4_adamw(plan.table_ptr, plan.chunks, plan.state_bits, plan.control_ptr, lr, lr_device, plan.betas[0],
+        status = load().nvfp4_adamw(plan.table_ptr, plan.chunks, plan.state_bits, plan.control_ptr, float(lr), lr_device, plan.betas[0],
                                     plan.betas[1], plan.eps, plan.seed, scale, plan.amax_ptr, plan.count, _raw(stream, plan.device))
         if status:
             _check(status, "nvfp4_adamw")

@@ -139,6 +139,44 @@ def test_any_alignment_and_nothing_outside_is_written(gpu, rows, cols, xt, offse
                     take(db, torch.float32, 4, cols)), dy, x, w, got.mean, got.rstd, xt, "f32")
 
 
+@pytest.mark.parametrize("rows,cols", [(7, 64), (5, 1024), (3, 1003)])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_operands_at_different_places_within_16_bytes(gpu, rows, cols, xt):
+    """x on a boundary, y and dx one element past one, dy two: no common shift."""
+    x, w, b, dy = make(rows, cols, xt, "f32", seed=6)
+    n = rows * cols
+    past = lambda k: torch.zeros(n + 8, dtype=TYPES[xt], device="cuda")[k:k + n]  # noqa: E731
+    y, dx, g = past(1), past(1), past(2)
+    g.copy_(dy.reshape(-1))
+    mean, rstd, top = (torch.empty(k, device="cuda") for k in (rows, rows, 1))
+    nv.nvfp4_layer_norm(x, CODE[xt], w, b, nv.TYPE_F32, rows, cols, 1e-5, y, mean, rstd, top)
+    check_forward(nv.Normed(y.view(rows, cols), mean, rstd, top), x, w, b, 1e-5, xt)
+    size = nv.nvfp4_layer_norm_workspace(rows, cols)
+    dw, db, work = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda"), torch.empty(size, dtype=torch.uint8, device="cuda")
+    nv.nvfp4_layer_norm_backward(g, x, CODE[xt], w, nv.TYPE_F32, mean, rstd, rows, cols, dx, dw, db, work, size)
+    # one column a thread and a slab of rows each: the chain is the slab's rows and the slabs
+    check_backward((dx.view(rows, cols), dw, db), dy, x, w, mean, rstd, xt, "f32")
+
+
+def test_two_streams_at_once(gpu):
+    """Two calls that overlap on the GPU, each with its own memory, give what they give alone."""
+    made = [make(2000, 1024, "bf16", "bf16", seed=k) for k in range(2)]
+    alone = []
+    for x, w, b, dy in made:
+        r = nv.layer_norm_forward(x, w, b, with_amax=True)
+        alone.append(tuple(r) + nv.layer_norm_backward(dy, x, w, r.mean, r.rstd))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[], []]
+    for turn in range(4):
+        for k, (x, w, b, dy) in enumerate(made):
+            r = nv.layer_norm_forward(x, w, b, with_amax=True, stream=streams[k])
+            got[k] = tuple(r) + nv.layer_norm_backward(dy, x, w, alone[k][1], alone[k][2], stream=streams[k])
+    torch.cuda.synchronize()
+    for a, g in zip(alone, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, g))
+
+
 def test_a_large_offset_cancels_nothing(gpu):
     """Values of deviation 1 around 4096 in FP32: mean and variance keep their digits."""
     x, w, b, _ = make(6, 4096, "f32", "f32", shift=0.0)

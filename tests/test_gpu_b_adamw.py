@@ -309,6 +309,22 @@ def test_norm_that_is_not_finite(gpu, bad, want):
     assert scale.item() < 1
 
 
+def test_a_plan_of_another_kind_or_length_is_left_alone(gpu):
+    """The kernels look at the plan's header: a call that does not belong to it changes nothing."""
+    plan = make([100, 3000], "bf16", "bf16", 32, False)
+    keep = [t.clone() for t in (*plan.params, plan.exp_avg, plan.exp_avg_sq, plan.control)]
+    args = (plan.control, 1e-3, None, 0.9, 0.95, 1e-8, 0)
+    nv.nvfp4_adamw(plan.table, plan.chunks, 8, *args)
+    nv.nvfp4_adamw(plan.table, plan.chunks, 32, *args, amax=torch.zeros(1, device="cuda"), count=1)
+    grads = nv.gradient_list(plan.grads)
+    nv.nvfp4_adamw(grads.table, grads.chunks, 32, *args)
+    torch.cuda.synchronize()
+    for a, b in zip(keep, (*plan.params, plan.exp_avg, plan.exp_avg_sq, plan.control)):
+        assert torch.equal(a, b)
+    nv.adamw(plan, 1e-3)
+    assert plan.steps() == 1 and not torch.equal(keep[1], plan.params[1])
+
+
 # ---- how it is called ----------------------------------------------------------------------------
 
 def test_refusals(gpu):
