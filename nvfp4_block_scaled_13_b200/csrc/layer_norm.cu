@@ -14,10 +14,11 @@
 // Rows arrive ahead of their use through a ring in shared memory. Each thread copies (cp.async)
 // and later reads its own 16-byte units only, so the ring needs no barrier and no registers.
 //
-// A row that does not start on 16 bytes is read as if it began at the unit's boundary, `shift`
-// elements earlier, and its first and last units are masked. Groups take rows in steps whose
-// length in bytes is a multiple of 16, so a group's shift, and with it the columns of each
-// thread, stays the same: odd row lengths run on the same vector path.
+// A row that does not start on 16 bytes has a head of up to 7 elements, whole units, and a tail; the
+// first threads of its group take an element of each beside their units. Groups take rows in steps
+// whose length in bytes is a multiple of 16, so a group's head, and with it the columns of each
+// thread, stays the same: odd row lengths run on the same vector path. (8192 x 4095 in BF16: 30 us
+// forward and 57 backward; with masked first and last units, on which a whole group waits, 35 and 74.)
 //
 // The column sums of the backward pass stay in registers; each CTA writes one partial row to the
 // workspace and a second kernel adds the partial rows in order, so the result does not depend on
@@ -94,6 +95,12 @@ __device__ __forceinline__ void join_top(uint32_t& top, const uint4& w, bf16) {
 __device__ __forceinline__ void join_top(uint32_t& top, const uint4& w, float) {
     top = max(max(top, w.x & 0x7FFFFFFFu), max(w.y & 0x7FFFFFFFu, max(w.z & 0x7FFFFFFFu, w.w & 0x7FFFFFFFu)));
 }
+__device__ __forceinline__ void join_top(uint32_t& top, float2 v, bf16) {
+    join_top(top, make_uint4(to_bf16x2(v.x, v.y), 0u, 0u, 0u), bf16{});
+}
+__device__ __forceinline__ void join_top(uint32_t& top, float2 v, float) {
+    top = max(top, max(magnitude(v.x), magnitude(v.y)));
+}
 __device__ __forceinline__ uint32_t top_bits(uint32_t top, bf16) { return max(top << 16, top & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t top_bits(uint32_t top, float) { return top; }
 
@@ -109,88 +116,56 @@ __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The columns of a thread: unit q holds columns start(q) .. start(q) + E - 1, of which those with
-// their bit in mask(q) exist.
-template <typename T, int Q, bool SHIFTED>
+// The columns of a thread: unit q holds columns start(q) .. start(q) + E - 1, if the row has them.
+template <typename T, int Q>
 struct Columns {
     static constexpr int E = kUnit<T>;
-    static constexpr uint32_t kAll = (1u << E) - 1u;
     int base, stride, cols;
 
-    __device__ __forceinline__ Columns(int t, int lanes, int shift, int cols_) : base(t * E - shift), stride(lanes * E), cols(cols_) {}
+    __device__ __forceinline__ Columns(int t, int lanes, int head, int cols_) : base(t * E + head), stride(lanes * E), cols(cols_) {}
     __device__ __forceinline__ int start(int q) const { return base + q * stride; }
-    // Whether all columns of a unit exist (for cols >= E).
-    __device__ __forceinline__ bool whole(int q) const { return static_cast<unsigned>(start(q)) <= static_cast<unsigned>(cols - E); }
-    __device__ __forceinline__ uint32_t mask(int q) const {
-        const int c = start(q);
-        if (!SHIFTED) return c < cols ? kAll : 0u;
-        uint32_t m = kAll;
-        if (c < 0) m &= kAll << -c;
-        if (c + E > cols) m &= c >= cols ? 0u : kAll >> (c + E - cols);
-        return m;
+    __device__ __forceinline__ bool has(int q) const { return start(q) + E <= cols; }
+};
+
+// Elements in front of the first 16-byte boundary of the row at `p`.
+template <typename T>
+__device__ __forceinline__ int head_of(uintptr_t p, int cols) {
+    return min(cols, static_cast<int>((0 - p & 15) / sizeof(T)));
+}
+
+// A thread's share of the head and the tail of a shifted row: one element of each, if there is one.
+template <typename T, bool SHIFTED>
+struct Edge {
+    bool any;        // for most threads there is none, and whole warps skip what is done about it
+    bool has[2];
+    int column[2];
+
+    __device__ __forceinline__ Edge(int t, int head, int cols) {
+        const int body = (cols - head) / kUnit<T> * kUnit<T>;
+        has[0] = SHIFTED && t < head;
+        has[1] = SHIFTED && t < cols - head - body;
+        any = has[0] || has[1];
+        column[0] = t;
+        column[1] = head + body + t;
+    }
+    __device__ __forceinline__ void load(const void* row, float2& v) const {
+        if (!SHIFTED) return;
+        v.x = has[0] ? to_float(static_cast<const T*>(row)[column[0]]) : 0.0f;
+        v.y = has[1] ? to_float(static_cast<const T*>(row)[column[1]]) : 0.0f;
+    }
+    __device__ __forceinline__ float2 param(const void* p, bool f32, float fill) const;
+    // Zero in the place of an element that does not exist.
+    __device__ __forceinline__ float2 keep(float2 v) const { return make_float2(has[0] ? v.x : 0.0f, has[1] ? v.y : 0.0f); }
+    __device__ __forceinline__ void store(void* row, float2 v) const {
+        if (has[0]) static_cast<T*>(row)[column[0]] = from_float<T>(v.x);
+        if (has[1]) static_cast<T*>(row)[column[1]] = from_float<T>(v.y);
     }
 };
 
 template <int H>
-__device__ __forceinline__ void keep(float2 (&v)[H], uint32_t mask) {
+__device__ __forceinline__ void keep_if(bool has, float2 (&v)[H]) {
 #pragma unroll
-    for (int k = 0; k < H; ++k) {
-        if (!(mask >> (2 * k) & 1u)) v[k].x = 0.0f;
-        if (!(mask >> (2 * k + 1) & 1u)) v[k].y = 0.0f;
-    }
-}
-
-// A row operand as one thread sees it: the address of its unit 0 in the row that comes next. A
-// unit that reaches over the tensor's ends (only where the tensor itself is not aligned) is copied
-// by the element.
-template <typename T, int Q, bool SHIFTED>
-struct Source {
-    const char *next, *begin, *end;
-
-    __device__ __forceinline__ Source(const void* tensor, int64_t rows, int64_t first, const Columns<T, Q, SHIFTED>& at)
-        : begin(static_cast<const char*>(tensor)), end(begin + rows * at.cols * int64_t(sizeof(T))) {
-        next = begin + (first * at.cols + at.start(0)) * int64_t(sizeof(T));
-    }
-    __device__ __forceinline__ void fetch(int q, uint32_t unit_bytes, uint32_t slot, uint32_t mask) const {
-        constexpr int E = kUnit<T>;
-        const char* from = next + q * unit_bytes;
-        if (mask == Columns<T, Q, SHIFTED>::kAll) {
-            copy_async(slot, from);
-        } else if (SHIFTED && mask) {
-            if (from >= begin && from + 16 <= end) {
-                copy_async(slot, from);
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    if (!(mask >> j & 1u)) continue;
-                    if (E == 8) {
-                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(slot + 2 * j), "h"(reinterpret_cast<const uint16_t*>(from)[j]) : "memory");
-                    } else {
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 4 * j), "r"(reinterpret_cast<const uint32_t*>(from)[j]) : "memory");
-                    }
-                }
-            }
-        }
-    }
-};
-
-template <typename T>
-__device__ __forceinline__ void store_unit(void* to, const uint4& w, uint32_t mask) {
-    constexpr int E = kUnit<T>;
-    if (mask == (1u << E) - 1u) {
-        *reinterpret_cast<uint4*>(to) = w;
-    } else if (mask) {
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            if (!(mask >> j & 1u)) continue;
-            if (E == 8) {
-                reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(a[j / 2] >> (16 * (j & 1)));
-            } else {
-                reinterpret_cast<uint32_t*>(to)[j] = a[j & 3];
-            }
-        }
-    }
+    for (int k = 0; k < H; ++k) v[k] = has ? v[k] : make_float2(0.0f, 0.0f);
 }
 
 __device__ __forceinline__ float param_at(const void* p, bool f32, int c) {
@@ -198,14 +173,13 @@ __device__ __forceinline__ float param_at(const void* p, bool f32, int c) {
 }
 
 // The weight's (or bias's) values of a unit; `fill` in every existing column where there is no
-// parameter, zero in columns that do not exist.
+// parameter, zero in a unit that does not exist.
 template <int E>
-__device__ __forceinline__ void load_param(const void* p, bool f32, bool vector, int c, uint32_t mask, float fill,
-                                           float2 (&out)[E / 2]) {
+__device__ __forceinline__ void load_param(const void* p, bool f32, bool vector, int c, bool has, float fill, float2 (&out)[E / 2]) {
     float v[E];
-    if (p == nullptr || mask != (1u << E) - 1u || !vector) {
+    if (p == nullptr || !has || !vector) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) v[j] = mask >> j & 1u ? (p ? param_at(p, f32, c + j) : fill) : 0.0f;
+        for (int j = 0; j < E; ++j) v[j] = has ? (p ? param_at(p, f32, c + j) : fill) : 0.0f;
     } else if (f32) {
 #pragma unroll
         for (int k = 0; k < E / 4; ++k) {
@@ -221,6 +195,11 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, bool vector,
     }
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) out[k] = make_float2(v[2 * k], v[2 * k + 1]);
+}
+
+template <typename T, bool SHIFTED>
+__device__ __forceinline__ float2 Edge<T, SHIFTED>::param(const void* p, bool f32, float fill) const {
+    return make_float2(has[0] ? (p ? param_at(p, f32, column[0]) : fill) : 0.0f, has[1] ? (p ? param_at(p, f32, column[1]) : fill) : 0.0f);
 }
 
 // ---- sums over a row's threads ------------------------------------------------------------
@@ -340,19 +319,19 @@ constexpr int kBackwardStages = 3;
 // Registers of a thread, and with them the CTAs that an SM holds (each of its four quarters has
 // 16384 registers).
 constexpr int forward_registers(int elements) { return elements == 16 ? 80 : 64; }
-constexpr int backward_registers(int elements) { return elements == 16 ? 128 : 80; }
+constexpr int kBackwardRegisters = 128;
 constexpr int resident(int registers, int threads) {
     return std::max(1, std::min(32, 16384 / (registers * 32) * 4 / (threads / 32)));
 }
 
 // Which rows a thread's group takes: the groups of a CTA take every ctas-th row in turn, which gives
-// all of them one shift.
+// all of them one head.
 template <typename T, int LANES, bool SHIFTED>
 struct Group {
     int lanes, t, groups, index;
     int64_t first, step;
     int turns, rows;   // turns of the CTA's loop (the shuffles need every lane of a warp), rows of the group
-    int shift;
+    int head;
     int part;          // index of the CTA, or cluster, and of its partial row
 
     __device__ __forceinline__ Group(const void* x, int64_t all_rows, int cols, int row_threads) {
@@ -375,7 +354,7 @@ struct Group {
         step = ctas * groups;
         turns = static_cast<int>((all_rows - base + step - 1) / step);
         rows = first < all_rows ? static_cast<int>((all_rows - first + step - 1) / step) : 0;
-        shift = SHIFTED ? static_cast<int>(((reinterpret_cast<uintptr_t>(x) + first * cols * int64_t(sizeof(T))) & 15) / sizeof(T)) : 0;
+        head = SHIFTED ? head_of<T>(reinterpret_cast<uintptr_t>(x) + first * cols * int64_t(sizeof(T)), cols) : 0;
     }
 };
 
@@ -383,27 +362,29 @@ struct Group {
 template <typename T, int N, int LANES, bool SHIFTED>
 __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid_constant__ NormArgs a) {
     constexpr int E = kUnit<T>, Q = N / E, H = E / 2, S = kForwardStages;
-    constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
     extern __shared__ uint4 ring[];   // [S][Q][threads]
     __shared__ WarpSums<LANES> warp_sums;
     const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols, a.row_threads);
-    const Columns<T, Q, SHIFTED> at(group.t, group.lanes, group.shift, a.cols);
-    uint32_t mask[Q];
+    const Columns<T, Q> at(group.t, group.lanes, group.head, a.cols);
+    const Edge<T, SHIFTED> edge(group.t, group.head, a.cols);
+    bool has[Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) mask[q] = at.mask(q);
+    for (int q = 0; q < Q; ++q) has[q] = at.has(q);
     const uint32_t unit_bytes = group.lanes * 16u, slot_bytes = blockDim.x * 16u;
     const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
     const uint32_t slots_end = slots + S * Q * slot_bytes;
     const int64_t row_bytes = group.step * a.cols * int64_t(sizeof(T));
-    Source<T, Q, SHIFTED> x(a.x, a.rows, group.first, at);
+    const char* row = static_cast<const char*>(a.x) + group.first * a.cols * int64_t(sizeof(T));   // for the edges
+    const char* next = row + at.start(0) * int(sizeof(T));
     int ahead = 0;   // rows whose copy has been started
     const auto fetch = [&](uint32_t slot) {
         if (ahead < group.rows) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) x.fetch(q, unit_bytes, slot + q * slot_bytes, mask[q]);
+            for (int q = 0; q < Q; ++q)
+                if (has[q]) copy_async(slot + q * slot_bytes, next + q * unit_bytes);
         }
         ++ahead;
-        x.next += row_bytes;
+        next += row_bytes;
         commit_copies();
     };
 #pragma unroll
@@ -411,15 +392,19 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
     float2 w[Q][H], b[Q][H];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), mask[q], 1.0f, w[q]);
-        load_param<E>(a.bias, a.w_f32, a.w_vector, at.start(q), mask[q], 0.0f, b[q]);
+        load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), has[q], 1.0f, w[q]);
+        load_param<E>(a.bias, a.w_f32, a.w_vector, at.start(q), has[q], 0.0f, b[q]);
     }
+    const float2 edge_w = edge.param(a.weight, a.w_f32, 1.0f), edge_b = edge.param(a.bias, a.w_f32, 0.0f);
+    float2 edge_next = make_float2(0.0f, 0.0f);
+    if (group.rows > 0) edge.load(row, edge_next);
     if (LANES <= 0) {
         warp_sums.clear();
         sync_all<LANES>();
     }
     const float inv = 1.0f / static_cast<float>(a.cols), eps = a.eps;
-    char* y = static_cast<char*>(a.y) + (group.first * a.cols + at.start(0)) * int64_t(sizeof(T));
+    char* y = static_cast<char*>(a.y) + group.first * a.cols * int64_t(sizeof(T));
+    const int y_first = at.start(0) * int(sizeof(T));
     const bool stats = group.t == 0 && (a.mean || a.rstd), tops = a.amax;
     uint32_t top = 0;
     uint32_t slot = slots, refill = slots + (S - 1) * Q * slot_bytes;
@@ -430,9 +415,15 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             unpack(read_shared(slot + q * slot_bytes), v[q], T{});
-            if (mask[q] != kAll) keep(v[q], mask[q]);
+            keep_if(has[q], v[q]);
 #pragma unroll
             for (int k = 0; k < H; ++k) sum2[k & 1] = add2(sum2[k & 1], v[q][k]);
+        }
+        float2 e = edge_next;
+        if (SHIFTED && edge.any) {
+            sum2[0] = add2(sum2[0], e);
+            row += row_bytes;
+            if (turn + 1 < group.rows) edge.load(row, edge_next);
         }
         fetch(refill);
         refill = slot;
@@ -451,9 +442,13 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
         for (int q = 0; q < Q; ++q) {
 #pragma unroll
             for (int k = 0; k < H; ++k) v[q][k] = add2(v[q][k], make_float2(-mean, -mean));
-            if (mask[q] != kAll) keep(v[q], mask[q]);
+            keep_if(has[q], v[q]);
 #pragma unroll
             for (int k = 0; k < H; ++k) square2[k & 1] = fma2(v[q][k], v[q][k], square2[k & 1]);
+        }
+        if (SHIFTED && edge.any) {
+            e = edge.keep(add2(e, make_float2(-mean, -mean)));
+            square2[0] = fma2(e, e, square2[0]);
         }
         square2[0] = add2(square2[0], square2[1]);
         float square = lane_sum<LANES>(square2[0].x + square2[0].y);
@@ -470,7 +465,12 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
                 for (int k = 0; k < H; ++k) v[q][k] = fma2(mul2(v[q][k], make_float2(rstd, rstd)), w[q][k], b[q][k]);
                 const uint4 out = pack(v[q], T{});
                 if (tops) join_top(top, out, T{});   // columns that do not exist hold zero
-                store_unit<T>(y + q * unit_bytes, out, mask[q]);
+                if (has[q]) *reinterpret_cast<uint4*>(y + y_first + q * unit_bytes) = out;
+            }
+            if (SHIFTED && edge.any) {
+                e = fma2(mul2(e, make_float2(rstd, rstd)), edge_w, edge_b);
+                if (tops) join_top(top, e, T{});
+                edge.store(y, e);
             }
             if (stats) {
                 const int64_t r = group.first + turn * group.step;
@@ -487,9 +487,10 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
 // Rows of 257 to 10240 columns. With few elements a thread, the two reductions, the barriers and
 // the loop cost more instructions than the elements do and bound the kernel (measured at 8192 x
 // 4096 in BF16: 16.6 instructions an element and 29 us with 16 elements a thread). Here a row
-// belongs to WARPS warps with N elements a lane, one CTA of 16 warps has an SM to itself (as many row groups as fit),  and
-// weight and bias stay in its shared memory as binary32, so that registers hold nothing but the
-// row. The row groups of a CTA take every gridDim.x-th row, which gives all of them one shift.
+// belongs to WARPS warps with N elements a lane, one CTA of 16 warps has
+// an SM to itself (as many row groups as fit), and weight and bias stay in its shared memory as
+// binary32, so that registers hold nothing but the row. The row groups of a CTA take every
+// gridDim.x-th row, which gives all of them one head.
 template <int WARPS>
 constexpr int kWideThreads = 16 / WARPS * WARPS * 32;   // whole row groups
 template <typename T, int Q>
@@ -497,70 +498,62 @@ constexpr int kWideStages = Q <= 2 ? 4 : sizeof(T) == 2 || Q <= 8 ? 2 : 1;   // 
 template <typename T, int Q>
 constexpr int kWideCtas = Q * 16 <= 32 ? 2 : 1;                           // CTAs of an SM
 
-// Q units a lane, of which the units from K on and, in a shifted row, unit 0 may hold columns that
-// do not exist.
+// Q units a lane, of which those from K on may not exist.
 template <typename T, int Q, int K, int WARPS, bool SHIFTED>
 __global__ void __launch_bounds__(kWideThreads<WARPS>, kWideCtas<T, Q>) norm_kernel(const __grid_constant__ NormArgs a) {
     constexpr int E = kUnit<T>, H = E / 2, P = E / 4, S = kWideStages<T, Q>;
     constexpr int kUnits = WARPS * 32 * Q, kGroups = 16 / WARPS;
-    constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll, kSlot = 512, kStage = Q * kSlot;
+    constexpr uint32_t kSlot = 512, kStage = Q * kSlot;
     extern __shared__ uint4 ring[];   // rows [warp][S][Q][lane], then weight [P][kUnits], bias [P][kUnits]
     __shared__ float sums[2][kGroups][WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp / WARPS, t = (warp % WARPS) * 32 + lane;
     float4* weights = reinterpret_cast<float4*>(ring + 16 * S * Q * 32);
     float4* biases = weights + P * kUnits;
     const uintptr_t place = reinterpret_cast<uintptr_t>(a.x) + blockIdx.x * (a.cols * uintptr_t(sizeof(T)));
-    const int shift = SHIFTED ? static_cast<int>((place & 15) / sizeof(T)) : 0;
-    const Columns<T, Q, SHIFTED> at(t, WARPS * 32, shift, a.cols);
-    const auto may_lack = [](int q) { return q >= K || (SHIFTED && q == 0); };
-    const bool lacks = !at.whole(0) || !at.whole(Q - 1);   // whether any of the lane's columns does not exist
+    const int head = SHIFTED ? head_of<T>(place, a.cols) : 0;
+    const Columns<T, Q> at(t, WARPS * 32, head, a.cols);
+    const Edge<T, SHIFTED> edge(t, head, a.cols);
+    const auto has = [&](int q) { return q < K || at.has(q); };
     const int64_t first = blockIdx.x + int64_t(group) * gridDim.x, step = int64_t(gridDim.x) * kGroups;
     const int rows = first < a.rows ? static_cast<int>((a.rows - first + step - 1) / step) : 0;
     const int64_t row_bytes = step * a.cols * int64_t(sizeof(T));
     constexpr uint32_t kUnitBytes = WARPS * 512;
 
-    Source<T, Q, SHIFTED> x(a.x, a.rows, first, at);
+    const char* row = static_cast<const char*>(a.x) + first * a.cols * int64_t(sizeof(T));   // for the edges
+    const char* next = row + at.start(0) * int(sizeof(T));
     const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * (S * kStage) + lane * 16u;
     int ahead = 0;
     const auto fetch = [&](uint32_t slot) {
         if (ahead < rows) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                    x.fetch(q, kUnitBytes, slot + q * kSlot, at.whole(q) ? kAll : at.mask(q));
-            }
+            for (int q = 0; q < Q; ++q)
+                if (has(q)) copy_async(slot + q * kSlot, next + q * kUnitBytes);
         }
         ++ahead;
-        x.next += row_bytes;
+        next += row_bytes;
         commit_copies();
     };
 #pragma unroll
     for (int s = 0; s < S; ++s) fetch(slots + s * kStage);
     for (int u = threadIdx.x; u < kUnits; u += kWideThreads<WARPS>) {
-        const Columns<T, 1, SHIFTED> one(u, 0, shift, a.cols);
+        const Columns<T, 1> one(u, 0, head, a.cols);
         float2 w[H], b[H];
-        load_param<E>(a.weight, a.w_f32, a.w_vector, one.start(0), one.mask(0), 1.0f, w);
-        load_param<E>(a.bias, a.w_f32, a.w_vector, one.start(0), one.mask(0), 0.0f, b);
+        load_param<E>(a.weight, a.w_f32, a.w_vector, one.start(0), one.has(0), 1.0f, w);
+        load_param<E>(a.bias, a.w_f32, a.w_vector, one.start(0), one.has(0), 0.0f, b);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             weights[p * kUnits + u] = make_float4(w[2 * p].x, w[2 * p].y, w[2 * p + 1].x, w[2 * p + 1].y);
             biases[p * kUnits + u] = make_float4(b[2 * p].x, b[2 * p].y, b[2 * p + 1].x, b[2 * p + 1].y);
         }
     }
+    const float2 edge_w = edge.param(a.weight, a.w_f32, 1.0f), edge_b = edge.param(a.bias, a.w_f32, 0.0f);
+    float2 edge_next = make_float2(0.0f, 0.0f);
+    if (rows > 0) edge.load(row, edge_next);
     __syncthreads();
     const float inv = 1.0f / static_cast<float>(a.cols), eps = a.eps;
-    char* y = static_cast<char*>(a.y) + (first * a.cols + at.start(0)) * int64_t(sizeof(T));
+    char* y = static_cast<char*>(a.y) + first * a.cols * int64_t(sizeof(T));
+    const int y_first = at.start(0) * int(sizeof(T));
     const bool stats = t == 0 && (a.mean || a.rstd), tops = a.amax;
-    // Zero in the place of a unit's columns that do not exist.
-    const auto drop = [&](int q, float2 (&u)[H]) {
-        if (!may_lack(q)) return;
-        if (SHIFTED) {
-            if (lacks) keep(u, at.mask(q));
-        } else {
-            const bool exists = at.start(q) < a.cols;
-#pragma unroll
-            for (int k = 0; k < H; ++k) u[k] = exists ? u[k] : make_float2(0.0f, 0.0f);
-        }
-    };
     // Sum over the row's warps; the two sets alternate as those of WarpSums do.
     const auto row_sum = [&](float v, int which) {
         v = warp_sum(v);
@@ -582,9 +575,15 @@ __global__ void __launch_bounds__(kWideThreads<WARPS>, kWideCtas<T, Q>) norm_ker
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             unpack(read_shared(slot + q * kSlot), v[q], T{});
-            drop(q, v[q]);
+            keep_if(has(q), v[q]);
 #pragma unroll
             for (int k = 0; k < H; ++k) part[k % 4] = add2(part[k % 4], v[q][k]);
+        }
+        float2 e = edge_next;
+        if (SHIFTED && edge.any) {
+            part[0] = add2(part[0], e);
+            row += row_bytes;
+            if (turn + 1 < rows) edge.load(row, edge_next);
         }
         fetch(slot);
         slot = S == 1 ? slot : slot == slots ? slots + kStage : slots;
@@ -595,9 +594,13 @@ __global__ void __launch_bounds__(kWideThreads<WARPS>, kWideCtas<T, Q>) norm_ker
         for (int q = 0; q < Q; ++q) {
 #pragma unroll
             for (int k = 0; k < H; ++k) v[q][k] = add2(v[q][k], make_float2(-mean, -mean));
-            drop(q, v[q]);
+            keep_if(has(q), v[q]);
 #pragma unroll
             for (int k = 0; k < H; ++k) square[k % 4] = fma2(v[q][k], v[q][k], square[k % 4]);
+        }
+        if (SHIFTED && edge.any) {
+            e = edge.keep(add2(e, make_float2(-mean, -mean)));
+            square[0] = fma2(e, e, square[0]);
         }
         square[0] = add2(add2(square[0], square[1]), add2(square[2], square[3]));
         const float rstd = rsqrtf(fmaf(row_sum(square[0].x + square[0].y, 1), inv, eps));
@@ -611,7 +614,12 @@ __global__ void __launch_bounds__(kWideThreads<WARPS>, kWideCtas<T, Q>) norm_ker
             }
             const uint4 out = pack(v[q], T{});
             if (tops) join_top(top, out, T{});   // columns that do not exist hold zero
-            store_unit<T>(y + q * kUnitBytes, out, may_lack(q) && lacks ? at.mask(q) : kAll);
+            if (has(q)) *reinterpret_cast<uint4*>(y + y_first + q * kUnitBytes) = out;
+        }
+        if (SHIFTED && edge.any) {
+            e = fma2(mul2(e, make_float2(rstd, rstd)), edge_w, edge_b);
+            if (tops) join_top(top, e, T{});
+            edge.store(y, e);
         }
         if (stats) {
             const int64_t r = first + turn * step;
@@ -680,20 +688,31 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
 // Adds the column sums of the row groups of a CTA, first those of a warp, and writes the CTA's
 // partial row. `shared`: [warps][cols].
 template <typename T, int Q, int LANES, bool SHIFTED>
-__device__ __forceinline__ void join_groups(float2 (&s)[Q][kUnit<T> / 2], const Columns<T, Q, SHIFTED>& at, float* shared, float* out) {
+__device__ __forceinline__ void join_groups(float2 (&s)[Q][kUnit<T> / 2], float2 edges, const Columns<T, Q>& at,
+                                            const Edge<T, SHIFTED>& edge, float* shared, float* out) {
     constexpr int E = kUnit<T>;
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();   // nobody uses the shared memory any more
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        const uint32_t mask = at.mask(q);
+        const bool has = at.has(q);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             float v = j & 1 ? s[q][j / 2].y : s[q][j / 2].x;
 #pragma unroll
             for (int off = LANES; off < 32; off *= 2) v += __shfl_xor_sync(kFull, v, off);
-            if (lane < LANES && (mask >> j & 1u)) shared[(threadIdx.x >> 5) * at.cols + at.start(q) + j] = v;
+            if (lane < LANES && has) shared[(threadIdx.x >> 5) * at.cols + at.start(q) + j] = v;
         }
+    }
+    if (SHIFTED) {
+#pragma unroll
+        for (int off = LANES; off < 32; off *= 2) {
+            edges.x += __shfl_xor_sync(kFull, edges.x, off);
+            edges.y += __shfl_xor_sync(kFull, edges.y, off);
+        }
+        float* sums = shared + (threadIdx.x >> 5) * at.cols;
+        if (lane < LANES && edge.has[0]) sums[edge.column[0]] = edges.x;
+        if (lane < LANES && edge.has[1]) sums[edge.column[1]] = edges.y;
     }
     __syncthreads();
     for (int c = threadIdx.x; c < at.cols; c += blockDim.x) {
@@ -720,49 +739,49 @@ __device__ __forceinline__ void join_rows(float2* s, const Rows& group, float2* 
 
 // A unit's column sums; `vector` where the partial rows lie as the operands' rows do.
 template <int E>
-__device__ __forceinline__ void store_sums(float* to, const float2 (&s)[E / 2], uint32_t mask, bool vector) {
+__device__ __forceinline__ void store_sums(float* to, const float2 (&s)[E / 2], bool vector) {
     if (vector) {
-        if (mask) {
 #pragma unroll
-            for (int k = 0; k < E / 4; ++k)
-                reinterpret_cast<float4*>(to)[k] = make_float4(s[2 * k].x, s[2 * k].y, s[2 * k + 1].x, s[2 * k + 1].y);
-        }
+        for (int k = 0; k < E / 4; ++k)
+            reinterpret_cast<float4*>(to)[k] = make_float4(s[2 * k].x, s[2 * k].y, s[2 * k + 1].x, s[2 * k + 1].y);
     } else {
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-            if (mask >> j & 1u) to[j] = j & 1 ? s[j / 2].y : s[j / 2].x;
+        for (int j = 0; j < E; ++j) to[j] = j & 1 ? s[j / 2].y : s[j / 2].x;
     }
 }
 
 template <typename T, int N, int LANES, bool SHIFTED>
-__global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
+__global__ void __maxnreg__(kBackwardRegisters) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     constexpr int E = kUnit<T>, Q = N / E, H = E / 2, P = E / 4, S = kBackwardStages;
-    constexpr uint32_t kAll = Columns<T, Q, SHIFTED>::kAll;
     extern __shared__ uint4 ring[];   // [S][Q][x, dy][threads], then the weight [P][Q][lanes of the CTA's rows]
     let_next_start();
     __shared__ WarpSums<LANES> sums1, sums2;
     const Group<T, LANES, SHIFTED> group(a.x, a.rows, a.cols, a.row_threads);
-    const Columns<T, Q, SHIFTED> at(group.t, group.lanes, group.shift, a.cols);
-    uint32_t mask[Q];
+    const Columns<T, Q> at(group.t, group.lanes, group.head, a.cols);
+    const Edge<T, SHIFTED> edge(group.t, group.head, a.cols);
+    bool has[Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) mask[q] = at.mask(q);
+    for (int q = 0; q < Q; ++q) has[q] = at.has(q);
     const uint32_t unit_bytes = group.lanes * 16u, slot_bytes = blockDim.x * 16u;
     const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
     const uint32_t slots_end = slots + S * Q * 2 * slot_bytes;
     const int64_t row_bytes = group.step * a.cols * int64_t(sizeof(T));
-    Source<T, Q, SHIFTED> x(a.x, a.rows, group.first, at), dy(a.dy, a.rows, group.first, at);
+    const int64_t first_byte = group.first * a.cols * int64_t(sizeof(T));
+    const char *x_row = static_cast<const char*>(a.x) + first_byte, *dy_row = static_cast<const char*>(a.dy) + first_byte;
+    const char *x = x_row + at.start(0) * int(sizeof(T)), *dy = dy_row + at.start(0) * int(sizeof(T));
     int ahead = 0;
     const auto fetch = [&](uint32_t slot) {
         if (ahead < group.rows) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                x.fetch(q, unit_bytes, slot + 2 * q * slot_bytes, mask[q]);
-                dy.fetch(q, unit_bytes, slot + (2 * q + 1) * slot_bytes, mask[q]);
+                if (!has[q]) continue;
+                copy_async(slot + 2 * q * slot_bytes, x + q * unit_bytes);
+                copy_async(slot + (2 * q + 1) * slot_bytes, dy + q * unit_bytes);
             }
         }
         ++ahead;
-        x.next += row_bytes;
-        dy.next += row_bytes;
+        x += row_bytes;
+        dy += row_bytes;
         commit_copies();
     };
 #pragma unroll
@@ -775,13 +794,13 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
         if constexpr (LANES > 0) {
             if (group.index == 0) {
                 float2 w[H];
-                load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), mask[q], 1.0f, w);
+                load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), has[q], 1.0f, w);
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     weights[(p * Q + q) * LANES] = make_float4(w[2 * p].x, w[2 * p].y, w[2 * p + 1].x, w[2 * p + 1].y);
             }
         } else {
-            load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), mask[q], 1.0f, held[q]);
+            load_param<E>(a.weight, a.w_f32, a.w_vector, at.start(q), has[q], 1.0f, held[q]);
         }
 #pragma unroll
         for (int k = 0; k < H; ++k) sw[q][k] = sb[q][k] = make_float2(0.0f, 0.0f);
@@ -792,12 +811,17 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
     }
     sync_all<LANES>();
     const float inv = 1.0f / static_cast<float>(a.cols);
-    char* dx = static_cast<char*>(a.dx) + (group.first * a.cols + at.start(0)) * int64_t(sizeof(T));
+    char* dx = static_cast<char*>(a.dx) + first_byte;
+    const int dx_first = at.start(0) * int(sizeof(T));
+    const float2 edge_w = edge.param(a.weight, a.w_f32, 1.0f);
+    float2 edge_x = make_float2(0.0f, 0.0f), edge_dy = edge_x, edge_sw = edge_x, edge_sb = edge_x;
     const float *means = a.mean + group.first, *rstds = a.rstd + group.first;
     float next_mean = 0.0f, next_rstd = 0.0f;
     if (group.rows > 0) {
         next_mean = *means;
         next_rstd = *rstds;
+        edge.load(x_row, edge_x);
+        edge.load(dy_row, edge_dy);
     }
     uint32_t slot = slots, refill = slots + (S - 1) * Q * 2 * slot_bytes;
     const int turns = LANES > 0 ? group.turns : group.rows;   // a warp's lanes make the same turns
@@ -813,10 +837,8 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
             unpack(read_shared(slot + (2 * q + 1) * slot_bytes), h[q], T{});
 #pragma unroll
             for (int k = 0; k < H; ++k) xh[q][k] = mul2(add2(xh[q][k], make_float2(-mean, -mean)), make_float2(rstd, rstd));
-            if (mask[q] != kAll || !exists) {
-                keep(xh[q], exists ? mask[q] : 0u);
-                keep(h[q], exists ? mask[q] : 0u);
-            }
+            keep_if(has[q] && exists, xh[q]);
+            keep_if(has[q] && exists, h[q]);
 #pragma unroll
             for (int k = 0; k < H; ++k) {
                 sw[q][k] = fma2(h[q][k], xh[q][k], sw[q][k]);
@@ -829,6 +851,24 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
                 }
                 s1 = add2(s1, h[q][k]);
                 s2 = fma2(h[q][k], xh[q][k], s2);
+            }
+        }
+        float2 edge_xh = make_float2(0.0f, 0.0f), edge_h = edge_xh;
+        if (SHIFTED && edge.any) {
+            if (exists) {
+                edge_xh = edge.keep(mul2(add2(edge_x, make_float2(-mean, -mean)), make_float2(rstd, rstd)));
+                edge_h = edge_dy;
+            }
+            edge_sw = fma2(edge_h, edge_xh, edge_sw);
+            edge_sb = add2(edge_sb, edge_h);
+            edge_h = mul2(edge_h, edge_w);
+            s1 = add2(s1, edge_h);
+            s2 = fma2(edge_h, edge_xh, s2);
+            x_row += row_bytes;
+            dy_row += row_bytes;
+            if (turn + 1 < group.rows) {
+                edge.load(x_row, edge_x);
+                edge.load(dy_row, edge_dy);
             }
         }
         fetch(refill);
@@ -857,8 +897,10 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
 #pragma unroll
                 for (int k = 0; k < H; ++k)
                     h[q][k] = mul2(add2(h[q][k], fma2(xh[q][k], make_float2(t2, t2), make_float2(t1, t1))), make_float2(rstd, rstd));
-                store_unit<T>(dx + q * unit_bytes, pack(h[q], T{}), mask[q]);
+                if (has[q]) *reinterpret_cast<uint4*>(dx + dx_first + q * unit_bytes) = pack(h[q], T{});
             }
+            if (SHIFTED && edge.any)
+                edge.store(dx, mul2(add2(edge_h, fma2(edge_xh, make_float2(t2, t2), make_float2(t1, t1))), make_float2(rstd, rstd)));
         }
         dx += row_bytes;
     }
@@ -867,18 +909,29 @@ __global__ void __maxnreg__(backward_registers(N)) norm_grad_kernel(const __grid
         float* out = a.sums + int64_t(group.part) * a.cols;
         float* out_b = out + int64_t(a.parts) * a.cols;
         if (LANES > 0) {
-            join_groups<T, Q, LANES, SHIFTED>(sw, at, reinterpret_cast<float*>(ring), out);
-            join_groups<T, Q, LANES, SHIFTED>(sb, at, reinterpret_cast<float*>(ring), out_b);
+            join_groups<T, Q, LANES, SHIFTED>(sw, edge_sw, at, edge, reinterpret_cast<float*>(ring), out);
+            join_groups<T, Q, LANES, SHIFTED>(sb, edge_sb, at, edge, reinterpret_cast<float*>(ring), out_b);
         } else {
             if (LANES == kRows) {   // onto the first group's, in the groups' order
                 join_rows<Q * H>(&sw[0][0], group, reinterpret_cast<float2*>(ring));
                 join_rows<Q * H>(&sb[0][0], group, reinterpret_cast<float2*>(ring));
+                if (SHIFTED) {
+                    join_rows<1>(&edge_sw, group, reinterpret_cast<float2*>(ring));
+                    join_rows<1>(&edge_sb, group, reinterpret_cast<float2*>(ring));
+                }
             }
             if (group.index == 0) {
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    store_sums<E>(out + at.start(q), sw[q], mask[q], !SHIFTED);
-                    store_sums<E>(out_b + at.start(q), sb[q], mask[q], !SHIFTED);
+                    if (!has[q]) continue;
+                    store_sums<E>(out + at.start(q), sw[q], !SHIFTED);
+                    store_sums<E>(out_b + at.start(q), sb[q], !SHIFTED);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!edge.has[e]) continue;
+                    out[edge.column[e]] = e ? edge_sw.y : edge_sw.x;
+                    out_b[edge.column[e]] = e ? edge_sb.y : edge_sb.x;
                 }
             }
         }
@@ -991,11 +1044,11 @@ struct Cut {
 };
 
 // Rows that start on 16 bytes take whole units; others, where all operands' rows start at the same
-// place within 16 bytes, are shifted.
+// place within 16 bytes, have heads and tails.
 Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent, bool backward) {
     const int unit = 16 / size;
     const bool shifted = !aligned || cols % unit != 0;
-    const int64_t need = cols + (shifted ? unit - 1 : 0);
+    const int64_t need = cols;
     if (!congruent) return {0, 0, 0, 1, 1, false};
     // backward one CTA an SM, so that few partial rows are left
     const int threads = backward ? 512 : 128;
@@ -1014,7 +1067,7 @@ Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent, bool backward
 }
 
 // Groups of CTAs (one, or a cluster) that share the rows: at most the `resident` ones, and so many
-// that all rows of one keep their shift: a multiple of `unit`, unless each has one row only.
+// that all rows of one keep their head: a multiple of `unit`, unless each has one row only.
 int64_t parts_of(const Cut& cut, int64_t rows, int64_t resident_ctas, int size) {
     const int64_t room = std::max<int64_t>(1, resident_ctas / cut.cluster), unit = 16 / size;
     return rows <= room ? rows : std::max<int64_t>(unit, room / unit * unit);
@@ -1027,7 +1080,7 @@ int64_t backward_parts(const Cut& cut, int64_t rows, int64_t cols, int size) {
         const int64_t across = (cols + 255) / 256;
         return std::min<int64_t>(rows, std::max<int64_t>(1, 4 * sms / across));
     }
-    return parts_of(cut, rows, sms * resident(backward_registers(cut.elements), cut.threads), size);
+    return parts_of(cut, rows, sms * resident(kBackwardRegisters, cut.threads), size);
 }
 
 // Launches a kernel with clusters of CTAs, and, where `after` is true, as one that may start
@@ -1109,8 +1162,7 @@ nvfp4_status launch_norm(const NormArgs& a, cudaStream_t stream) {
 }
 
 // Rows of WARPS warps whose lanes need FROM to 8 (BF16) units; FP32 rows need twice as many, in
-// coarser steps. A row whose shift happens to be 0 may end one unit earlier than the longest shift
-// would have it.
+// coarser steps. The units of a shifted row are up to two fewer.
 template <typename T, int WARPS, int FROM, bool SHIFTED>
 nvfp4_status launch_wide(const NormArgs& a, int need, cudaStream_t stream) {
     constexpr int S = SHIFTED;
@@ -1135,7 +1187,7 @@ nvfp4_status dispatch_norm(const NormArgs& a, const Cut& cut, cudaStream_t strea
     if (cut.lanes == 8) return launch_group<T, 8, 8, SHIFTED>(a, cut, stream);
     if (cut.lanes == 16) return launch_group<T, 8, 16, SHIFTED>(a, cut, stream);
     if (cut.lanes == 32 && cut.elements == 8) return launch_group<T, 8, 32, SHIFTED>(a, cut, stream);
-    const int need = a.cols + (SHIFTED ? kUnit<T> - 1 : 0);
+    const int need = a.cols;
     if (need <= 2048) return launch_wide<T, 1, 2, SHIFTED>(a, need, stream);
     if (need <= 4096) return launch_wide<T, 2, 5, SHIFTED>(a, need, stream);
     if (need <= 6144) return launch_wide<T, 3, 6, SHIFTED>(a, need, stream);
