@@ -6,7 +6,7 @@
 // 8-bit states took 420 us, against 377).
 //
 // An element costs, with BF16 gradients, 28 bytes with an FP32 master and 32-bit states: memory
-// bounds that step (168 M elements: 815 us, 88% of the copy bandwidth). A BF16 parameter with 8-bit
+// bounds that step (168 M elements: 798 us, 90% of the copy bandwidth). A BF16 parameter with 8-bit
 // states costs 10.125 bytes and 49 instructions: there the issue slots bound it (200 M elements:
 // 367 us, 84%). Hence paired (f32x2) arithmetic, three-operand maxima, addition of random bits in place
 // of a comparison, and rare cases (zero codes, NaN) behind one test for eight elements.
@@ -35,10 +35,11 @@ constexpr int kThreads = 256;
 constexpr int kTile = kThreads * 8;        // elements of one pass of a CTA: eight a thread
 constexpr uint32_t kMagic = 0x4E56504Cu;
 constexpr uint32_t kGolden = 0x9E3779B9u;
-// CTAs of an SM. 8-bit states need 80 registers (64 spill: 556 us for 200 M elements in place of 445
-// at that stage), 32-bit ones fit into 64.
-template <bool EIGHT>
-constexpr int kStepCtas = EIGHT ? 3 : 4;
+// CTAs of an SM in a step. 8-bit states need 80 registers: with 64, for four CTAs, they spill (556 us
+// for 200 M elements in place of 445 at that stage). 32-bit states fit into 64, but four CTAs stream
+// from too many places at once: 168 M elements with masters took 835 us with four, 798 with three
+// and 863 with two.
+constexpr int kStepCtas = 3;
 constexpr int kNormCtas = 4;
 // Ring of each CTA (8-bit states), as much as three CTAs can have: 200 M elements took 464 us with
 // three tiles in it, 431 with four, and 381 with five and the ranges above.
@@ -712,7 +713,7 @@ __device__ __forceinline__ void publish_top(uint32_t& top, bool halves, uint32_t
 }
 
 template <bool EIGHT>
-__global__ void __launch_bounds__(kThreads, kStepCtas<EIGHT>) adamw_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kThreads, kStepCtas) adamw_kernel(const StepArgs a) {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Image image(a.plan, a.chunks);
     Runs runs(a.chunks);
@@ -1116,10 +1117,10 @@ extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t st
         return NVFP4_ERR_CUDA;
     const StepArgs a{plan, static_cast<uint32_t>(chunks), control, lr, lr_device, beta1, beta2, eps, seed, scale, reinterpret_cast<uint32_t*>(amax), static_cast<uint32_t>(count)};
     if (state_bits == 32) {
-        adamw_kernel<false><<<resident_grid(chunks, kStepCtas<false>), kThreads, 0, stream>>>(a);
+        adamw_kernel<false><<<resident_grid(chunks, kStepCtas), kThreads, 0, stream>>>(a);
     } else {
         if (!allow_ring()) return NVFP4_ERR_CUDA;
-        adamw_kernel<true><<<resident_grid(chunks, kStepCtas<true>), kThreads, kRingBytes, stream>>>(a);
+        adamw_kernel<true><<<resident_grid(chunks, kStepCtas), kThreads, kRingBytes, stream>>>(a);
     }
     return launched();
 }
