@@ -202,6 +202,12 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, with_stats=
     return Normed(y, mean, rstd, top)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace(rows, cols, device):
+    """nvfp4_layer_norm_workspace on `device`, which is current."""
+    return load().nvfp4_layer_norm_workspace(rows, cols)
+
+
 def layer_norm_backward(dy, x, weight, mean, rstd, with_weight=True, with_bias=True, stream=None):
     """(dx, dweight, dbias) of layer norm from its input and the statistics of its forward pass.
     dweight and dbias have the weight's type (FP32 without one); None where not asked for."""
@@ -221,7 +227,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, with_weight=True, with_bias=T
         if with_bias:
             dbias = _torch.empty(cols, dtype=dtype, device=device)
         if with_weight or with_bias:
-            size = load().nvfp4_layer_norm_workspace(rows, cols)
+            size = _workspace(rows, cols, device.index)
             work = _torch.empty(size, dtype=_torch.uint8, device=device)
         status = load().nvfp4_layer_norm_backward(*sources, x_type, w, w_type, _address(mean), _address(rstd), rows, cols, dx.data_ptr(),
                                                   dweight.data_ptr() if with_weight else None, dbias.data_ptr() if with_bias else None,
@@ -399,6 +405,7 @@ def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=
             records.append(record)
         plan = AdamWPlan(grads, device, records)
         plan.params, plan.offsets, plan.numels = params, offsets, [p.numel() for p in params]
+        plan.versioned = [p for p in params if p.requires_grad or p.grad_fn is not None]
         plan.state_bits, plan.betas, plan.eps, plan.seed = state_bits, (float(betas[0]), float(betas[1])), float(eps), seed
         plan.master, plan.exp_avg, plan.exp_avg_sq = master, flat["exp_avg"], flat["exp_avg_sq"]
         plan.exp_avg_scale, plan.exp_avg_sq_scale = flat.get("exp_avg_scale"), flat.get("exp_avg_sq_scale")
@@ -428,7 +435,7 @@ def grad_norm(grads: GradientList, max_norm: float = math.inf, stream=None):
 
 
 def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
-    """One AdamW step, in place. ``lr``: a number, or an FP32 [1] tensor that the kernel reads (a
+    """One AdamW step, in place (autograd's graphs that saved a parameter notice). ``lr``: a number, or an FP32 [1] tensor that the kernel reads (a
     captured call then follows it; the count of steps is kept on the device anyway). ``scale``:
     an FP32 [1] factor of the gradients, as ``grad_norm`` gives it."""
     if not isinstance(plan, AdamWPlan):
@@ -445,3 +452,5 @@ def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
                                     plan.betas[1], plan.eps, plan.seed, scale, plan.amax_ptr, plan.count, _raw(stream, plan.device))
         if status:
             _check(status, "nvfp4_adamw")
+    if plan.versioned:
+        _torch.autograd.graph.increment_version(plan.versioned)

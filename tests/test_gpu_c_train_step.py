@@ -119,6 +119,17 @@ def test_inference_run_feeds_the_tensor_core_product(gpu):
         assert torch.equal(nv.gemm(a, wq), nv.gemm(b, wq))
 
 
+def test_a_graph_that_saved_a_parameter_notices_the_step(gpu):
+    p = torch.randn(64, device="cuda", requires_grad=True)
+    p.grad = torch.zeros_like(p)
+    plan = nv.adamw_plan([p], [p.grad])
+    y = (p * p).sum()
+    y.backward(retain_graph=True)
+    nv.adamw(plan, 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
 def test_a_step_leaves_no_memory_behind(gpu):
     """Without the cycle collector: what the norm, the clip and the step allocate is free after them."""
     s = Student(32, True)
