@@ -43,8 +43,9 @@ typedef enum {
  * The variance is the mean square distance from the mean, taken from the row held on chip, so
  * a large mean cancels nothing. Every pointer needs its element's alignment only; x and y are
  * best at the same place within 16 bytes. cols >= 1 and rows >= 0 (else NVFP4_ERR_SHAPE), eps
- * finite and >= 0 (else NVFP4_ERR_VALUE). One kernel, one read of x (rows of more than 65536
- * columns, and operands that start at different places within 16 bytes, are read again from L2), after a zero-fill of amax where more than one CTA runs. */
+ * finite and >= 0 (else NVFP4_ERR_VALUE). One kernel, one read of x (rows of more
+ * than 65536 columns, and operands that start at different places within 16 bytes, are read
+ * again from L2), after a zero-fill of amax where more than one CTA runs. */
 NVFP4_API nvfp4_status nvfp4_layer_norm(const void* x, nvfp4_type x_type, const void* weight, const void* bias,
                                         nvfp4_type w_type, int64_t rows, int64_t cols, float eps, void* y,
                                         float* mean, float* rstd, float* amax, cudaStream_t stream);

@@ -228,6 +228,7 @@ struct Factors {
 // The step's factors, and for each warp the description of the tensor that it works on: in shared
 // memory, because registers are scarce below, and at file scope, so that every function knows it.
 __shared__ Factors factors;
+__shared__ nvfp4_adamw_control counted;   // the control block after this step
 __shared__ Tensor tensors[kThreads / 32];
 
 struct StepArgs {
@@ -736,10 +737,15 @@ __global__ void __launch_bounds__(kThreads, kStepCtas) adamw_kernel(const StepAr
         f.rest2 = static_cast<float>(1.0 - a.beta2);
         f.eps = a.eps;
         f.lr = a.lr_device ? *a.lr_device : a.lr;
-        f.rate = f.lr / static_cast<float>(1.0 - a.control->beta1_t * a.beta1);
-        f.root = 1.0f / sqrtf(static_cast<float>(1.0 - a.control->beta2_t * a.beta2));
+        nvfp4_adamw_control c = *a.control;
+        f.key = mix(a.seed + kGolden * c.step);
+        c.beta1_t *= a.beta1;
+        c.beta2_t *= a.beta2;
+        c.step += 1;
+        counted = c;
+        f.rate = f.lr / static_cast<float>(1.0 - c.beta1_t);
+        f.root = 1.0f / sqrtf(static_cast<float>(1.0 - c.beta2_t));
         f.scale = a.scale ? *a.scale : 1.0f;
-        f.key = mix(a.seed + kGolden * a.control->step);
         factors = f;
     }
     const Header header = *image.header;
@@ -791,10 +797,10 @@ __global__ void __launch_bounds__(kThreads, kStepCtas) adamw_kernel(const StepAr
     // arrives.
     __syncthreads();
     if (threadIdx.x == 0 && takes_place && atomicAdd(&a.control->arrived, 1u) == gridDim.x - 1) {
+        a.control->beta1_t = counted.beta1_t;
+        a.control->beta2_t = counted.beta2_t;
+        a.control->step = counted.step;
         a.control->arrived = 0;
-        a.control->step += 1;
-        a.control->beta1_t *= a.beta1;
-        a.control->beta2_t *= a.beta2;
     }
 }
 
