@@ -1070,7 +1070,7 @@ Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent, bool backward
 // Groups of CTAs (one, or a cluster) that share the rows: at most the `resident` ones, and so many
 // that all rows of one keep their head: a multiple of `unit`, unless each has one row only.
 int64_t parts_of(const Cut& cut, int64_t rows, int64_t resident_ctas, int size) {
-    const int64_t room = std::max<int64_t>(1, resident_ctas / cut.cluster), unit = 16 / size;
+    const int64_t room = std::max<int64_t>(1, resident_ctas / cut.cluster), unit = cut.shifted ? 16 / size : 1;
     return rows <= room ? rows : std::max<int64_t>(unit, room / unit * unit);
 }
 
