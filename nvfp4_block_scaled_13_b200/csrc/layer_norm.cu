@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(kWideThreads<WARPS>, kWideCtas<T, Q>) norm_ker
             if (turn + 1 < rows) edge.load(row, edge_next);
         }
         fetch(slot);
-        slot = S == 1 ? slot : slot == slots ? slots + kStage : slots;
+        slot += kStage;
+        if (slot == slots + S * kStage) slot = slots;
         part[0] = add2(add2(part[0], part[1]), add2(part[2], part[3]));
         const float mean = row_sum(part[0].x + part[0].y, 0) * inv;
         float2 square[4] = {};
