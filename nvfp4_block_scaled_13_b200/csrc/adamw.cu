@@ -469,8 +469,8 @@ __device__ __forceinline__ void step_tile_32(const nvfp4_opt_tensor& d, bool vec
                 w[1] = to_bf16x2(p[h].v[1].x, p[h].v[1].y);
                 write_four(static_cast<bf16*>(d.param), i, n, whole, make_uint2(w[0], w[1]));
             } else {
-                const uint32_t place = static_cast<uint32_t>((d.first + i) >> 2);
-                round_stochastic(p[h].v, mix((place >> 1) ^ f.key) + (place & 1u) * (4 * kGolden), w);
+                const int64_t place = d.first + i;   // below 2^35
+                round_stochastic(p[h].v, mix(static_cast<uint32_t>(place >> 3) ^ f.key) + (static_cast<uint32_t>(place) & 4u) * kGolden, w);
                 write_four(source, i, n, whole, make_uint2(w[0], w[1]));
             }
             join_stored(top, w[0], whole, i, n);
