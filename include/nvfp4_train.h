@@ -145,9 +145,9 @@ typedef struct {
  *   m' = fma(m, beta1, (1 - beta1) * g)
  *   v' = fma(v, beta2, (1 - beta2) * (g * g));   u' = sqrt(v')
  *   p' = fma(m' / fma(u', r, eps), -lr / (1 - beta1^t), p * (1 - lr * weight_decay)),  r = 1 / sqrt(1 - beta2^t)
- * where 1 - beta^t is taken in binary64 and rounded once. Beside 8-bit states the
+ * where 1 - beta^t is taken in binary64 and rounded once. Beside 8-bit states and with eps in [2^-36, 2^100] the
  * root is the hardware's approximation (2^-23; 0 for a v' below 2^-126) and the quotient the product with its approximate
- * reciprocal (2^-23).
+ * reciprocal (2^-23); any other eps, 0 among them, takes the rounded root and quotient.
  * Parameters. FP32: p. BF16 with a master: p is the master, param = BF16(p'), to nearest even.
  * BF16 without one: p' is rounded stochastically, because an update is mostly far below half a
  * BF16 step, and rounding to nearest would lose it every time.

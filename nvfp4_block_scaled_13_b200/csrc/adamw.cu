@@ -247,7 +247,11 @@ struct StepArgs {
 
 // Root and reciprocal beside 8-bit states, whose step is bound by the instructions: the hardware's
 // approximations (relative errors of at most 2^-23 each; a v below 2^-126 counts as 0). u is then
-// rounded to 4 bits, and the update is added to a parameter that it changes in its last bits.
+// rounded to 4 bits, and the update is added to a parameter that it changes in its last bits. A v
+// that counts as 0 takes up to 2^-63 from u, which an eps of at least kLeastEps hides (2^-27 of the
+// denominator); and the reciprocal of a denominator above 2^126 is 0. Any other eps, 0 among them, takes
+// the rounded root and quotient in their place (ROUNDED below).
+constexpr float kLeastEps = 0x1p-36f, kMostEps = 0x1p100f;
 __device__ __forceinline__ float approximate_root(float v) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -597,7 +601,7 @@ struct Write {
 };
 
 // The step of a thread's eight elements, of which `left` exist where not all do; the maximum of the stored parameters is joined to `top`.
-template <uint32_t KIND>
+template <uint32_t KIND, bool ROUNDED>
 __device__ __forceinline__ void step_eight(const Write<KIND>& to, const Read<KIND>& r, bool whole, int64_t left, float keep,
                                            const Factors& f, uint32_t& top) {
     constexpr bool PARAM_F32 = KIND & kParamF32, MASTER = KIND & kMaster;
@@ -615,9 +619,10 @@ __device__ __forceinline__ void step_eight(const Write<KIND>& to, const Read<KIN
         m[k] = fma2(mul2(m[k], both(sm)), both(f.beta1), mul2(g[k], both(f.rest1)));
         u[k] = mul2(u[k], both(su));
         u[k] = fma2(mul2(u[k], u[k]), both(f.beta2), mul2(mul2(g[k], g[k]), both(f.rest2)));
-        u[k] = make_float2(approximate_root(u[k].x), approximate_root(u[k].y));
+        u[k] = ROUNDED ? make_float2(sqrtf(u[k].x), sqrtf(u[k].y)) : make_float2(approximate_root(u[k].x), approximate_root(u[k].y));
         const float2 under = fma2(u[k], both(f.root), both(f.eps));
-        const float2 ratio = mul2(m[k], make_float2(approximate_reciprocal(under.x), approximate_reciprocal(under.y)));
+        const float2 ratio = ROUNDED ? make_float2(m[k].x / under.x, m[k].y / under.y)
+                                     : mul2(m[k], make_float2(approximate_reciprocal(under.x), approximate_reciprocal(under.y)));
         p[k] = fma2(ratio, both(-f.rate), mul2(p[k], both(keep)));
     }
     const uint32_t word = mix(static_cast<uint32_t>(to.index >> 3) ^ f.key);
@@ -654,7 +659,7 @@ __device__ __forceinline__ void step_eight(const Write<KIND>& to, const Read<KIN
 // A run: whole tiles through the ring, then the tile in which the tensor ends, or all of it where a
 // pointer does not suit whole accesses. A function of its own for each kind: inlined side by side,
 // the kinds took registers from one another and spilled.
-template <uint32_t KIND>
+template <uint32_t KIND, bool ROUNDED>
 __device__ __noinline__ uint32_t step_run_8(bool vector, int64_t lo, int64_t hi, uint32_t top) {
     const nvfp4_opt_tensor& d = tensors[threadIdx.x >> 5].d;
     const Factors& f = factors;
@@ -682,14 +687,14 @@ __device__ __noinline__ uint32_t step_run_8(bool vector, int64_t lo, int64_t hi,
         stage = stage == S - 1 ? 0 : stage + 1;
         Read<KIND> now;
         now.collect(slot);
-        step_eight<KIND>(Write<KIND>(d, at), now, true, 8, keep, f, top);
+        step_eight<KIND, ROUNDED>(Write<KIND>(d, at), now, true, 8, keep, f, top);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     for (; at - threadIdx.x * 8 < hi; at += kTile) {
         Read<KIND> now;
         const bool eight = vector && at + 8 <= d.numel;
         now.fetch_from(d, at, eight);
-        step_eight<KIND>(Write<KIND>(d, at), now, eight, d.numel - at, keep, f, top);
+        step_eight<KIND, ROUNDED>(Write<KIND>(d, at), now, eight, d.numel - at, keep, f, top);
     }
     return top;
 }
@@ -713,7 +718,7 @@ __device__ __forceinline__ void publish_top(uint32_t& top, bool halves, uint32_t
     top = 0;
 }
 
-template <bool EIGHT>
+template <bool EIGHT, bool ROUNDED>
 __global__ void __launch_bounds__(kThreads, kStepCtas) adamw_kernel(const StepArgs a) {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Image image(a.plan, a.chunks);
@@ -774,12 +779,12 @@ __global__ void __launch_bounds__(kThreads, kStepCtas) adamw_kernel(const StepAr
         const bool vector = t.variant & kVector;
         if constexpr (EIGHT) {
             switch (t.variant & (kGradF32 | kParamF32 | kMaster)) {
-                case 0: top = step_run_8<0>(vector, lo, hi, top); break;
-                case kGradF32: top = step_run_8<kGradF32>(vector, lo, hi, top); break;
-                case kParamF32: top = step_run_8<kParamF32>(vector, lo, hi, top); break;
-                case kParamF32 | kGradF32: top = step_run_8<kParamF32 | kGradF32>(vector, lo, hi, top); break;
-                case kMaster: top = step_run_8<kMaster>(vector, lo, hi, top); break;
-                default: top = step_run_8<kMaster | kGradF32>(vector, lo, hi, top); break;
+                case 0: top = step_run_8<0, ROUNDED>(vector, lo, hi, top); break;
+                case kGradF32: top = step_run_8<kGradF32, ROUNDED>(vector, lo, hi, top); break;
+                case kParamF32: top = step_run_8<kParamF32, ROUNDED>(vector, lo, hi, top); break;
+                case kParamF32 | kGradF32: top = step_run_8<kParamF32 | kGradF32, ROUNDED>(vector, lo, hi, top); break;
+                case kMaster: top = step_run_8<kMaster, ROUNDED>(vector, lo, hi, top); break;
+                default: top = step_run_8<kMaster | kGradF32, ROUNDED>(vector, lo, hi, top); break;
             }
         } else {
             switch (t.variant & (kGradF32 | kParamF32 | kMaster)) {
@@ -1001,20 +1006,28 @@ unsigned resident_grid(int64_t chunks, int per_sm) {
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(chunks, int64_t(sm_count()) * per_sm)));
 }
 
-// Lets the step's kernel have its ring on the current device (once per device).
+// Lets a step's kernel have its ring on the current device (once per device).
+template <auto kernel>
 bool allow_ring() {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> allowed[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
     if (dev < kMaxDevices && allowed[dev].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(adamw_kernel<true>), cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) !=
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) !=
         cudaSuccess) {
         cudaGetLastError();
         return false;
     }
     if (dev < kMaxDevices) allowed[dev].store(true, std::memory_order_release);
     return true;
+}
+
+template <bool ROUNDED>
+nvfp4_status launch_step_8(const StepArgs& a, cudaStream_t stream) {
+    if (!allow_ring<adamw_kernel<true, ROUNDED>>()) return NVFP4_ERR_CUDA;
+    adamw_kernel<true, ROUNDED><<<resident_grid(a.chunks, kStepCtas), kThreads, kRingBytes, stream>>>(a);
+    return launched();
 }
 
 }  // namespace
@@ -1122,11 +1135,7 @@ extern "C" nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t st
     if (amax && count > 0 && cudaMemsetAsync(amax, 0, static_cast<size_t>(count) * 4, stream) != cudaSuccess)
         return NVFP4_ERR_CUDA;
     const StepArgs a{plan, static_cast<uint32_t>(chunks), control, lr, lr_device, beta1, beta2, eps, seed, scale, reinterpret_cast<uint32_t*>(amax), static_cast<uint32_t>(count)};
-    if (state_bits == 32) {
-        adamw_kernel<false><<<resident_grid(chunks, kStepCtas), kThreads, 0, stream>>>(a);
-    } else {
-        if (!allow_ring()) return NVFP4_ERR_CUDA;
-        adamw_kernel<true><<<resident_grid(chunks, kStepCtas), kThreads, kRingBytes, stream>>>(a);
-    }
+    if (state_bits == 8) return eps >= kLeastEps && eps <= kMostEps ? launch_step_8<false>(a, stream) : launch_step_8<true>(a, stream);
+    adamw_kernel<false, true><<<resident_grid(chunks, kStepCtas), kThreads, 0, stream>>>(a);
     return launched();
 }

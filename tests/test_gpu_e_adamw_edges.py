@@ -50,3 +50,34 @@ def test_random_words_follow_the_index_past_2_to_the_34(gpu, bits, first):
     if bits == 8:
         got["exp_avg_scale"], got["exp_avg_sq_scale"] = (raw(s) for s in scales)
     R.assert_step(got, want, bits)
+
+
+@pytest.mark.parametrize("param,masters", [("bf16", False), ("bf16", True), ("f32", False)])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-30, 1e-12, 1e31])
+def test_8_bit_states_with_an_eps_that_hides_nothing(gpu, param, masters, eps):
+    """Gradients whose squares are at and below the smallest normal number, and an eps that a root
+    flushed to zero would leave alone in the denominator: every bit is that of the rounded formula."""
+    n = 4096 + 50
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    g = torch.exp2(torch.rand(n, device="cuda", generator=gen) * 20 - 70) * torch.sign(torch.randn(n, device="cuda", generator=gen))
+    p = torch.randn(n, device="cuda", generator=gen).to(torch.bfloat16 if param == "bf16" else torch.float32)
+    plan = nv.adamw_plan([p], [g], state_bits=8, masters=masters, eps=eps, betas=(0.9, 0.95), weight_decay=0.1, seed=5)
+    for step in range(2):
+        state = {k: raw(t) for k, t in plan.state(0).items()}
+        old = values(plan.state(0)["master"] if masters else p).copy()
+        m = R.decode(state["exp_avg"], state["exp_avg_scale"])
+        root = R.decode(state["exp_avg_sq"], state["exp_avg_sq_scale"])
+        # the step of 32-bit states, whose root and quotient are rounded, from the decoded ones
+        want = R.adamw_bits(old, values(g), m, root * root, param_bf16=param == "bf16", master=masters, bits=32, lr=1e-3, decay=0.1,
+                            betas=(0.9, 0.95), eps=eps, scale=1.0, steps=step, first=0, seed=5)
+        nv.adamw(plan, 1e-3)
+        got = {k: raw(t) for k, t in plan.state(0).items()}
+        assert np.isfinite(values(p)).all() and (want["_root"] < 2.0 ** -63).any() and (want["_root"] > 0).all()
+        np.testing.assert_array_equal(values(p), want["param"])
+        if masters:
+            np.testing.assert_array_equal(got["master"], want["master"])
+        for name, (codes, scales) in (("exp_avg", R.encode_nearest(want["exp_avg"])),
+                                      ("exp_avg_sq", R.encode_stochastic(want["_root"], want["_word"]))):
+            np.testing.assert_array_equal(got[name], codes)
+            np.testing.assert_array_equal(got[name + "_scale"], scales)
+        assert (got["exp_avg_sq"] > 0).all(), "a positive root keeps a positive code"
