@@ -1043,7 +1043,7 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
     if (!count_chunks(tensors, count, &length, &chunks)) return NVFP4_ERR_SHAPE;
     if (image == nullptr || chunks_out == nullptr) return NVFP4_ERR_NULL;
     if (image_bytes < plan_bytes(count, chunks)) return NVFP4_ERR_SHAPE;
-    bool gradients = true;   // tensors without an element say nothing
+    bool gradients = true;
     for (int64_t i = 0; i < count; ++i)
         if (tensors[i].param != nullptr) gradients = false;
     int32_t bits = 0;
@@ -1054,14 +1054,16 @@ extern "C" nvfp4_status nvfp4_tensor_plan(const nvfp4_opt_tensor* tensors, int64
             if (!gradients && t.param == nullptr && t.numel > 0) return NVFP4_ERR_VALUE;
             const nvfp4_status st = check_tensor(t, gradients);
             if (st != NVFP4_OK) return st;
+            if (!gradients) {   // of tensors without an element too
+                if (bits != 0 && bits != t.state_bits) return NVFP4_ERR_VALUE;
+                bits = t.state_bits;
+            }
             if (t.numel == 0) continue;
             const auto add = [&](const void* p, int64_t bytes, bool written) {
                 if (p) spans.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
             };
             add(t.grad, t.numel * size_of(t.grad_type), false);
             if (gradients) continue;
-            if (bits != 0 && bits != t.state_bits) return NVFP4_ERR_VALUE;
-            bits = t.state_bits;
             add(t.param, t.numel * size_of(t.param_type), true);
             add(t.master, t.numel * 4, true);
             add(t.exp_avg, t.numel * t.state_bits / 8, true);

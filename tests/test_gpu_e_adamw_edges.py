@@ -81,3 +81,21 @@ def test_8_bit_states_with_an_eps_that_hides_nothing(gpu, param, masters, eps):
             np.testing.assert_array_equal(got[name], codes)
             np.testing.assert_array_equal(got[name + "_scale"], scales)
         assert (got["exp_avg_sq"] > 0).all(), "a positive root keeps a positive code"
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_list_of_empty_tensors_counts_its_steps(gpu, bits):
+    """Through the C entry points (the wrapper refuses such a list)."""
+    memory = torch.full((64,), 3.0, device="cuda")
+    at = memory.data_ptr()
+    array = (nv.OptTensor * 1)(nv.OptTensor(param=at, grad=at, exp_avg=at, exp_avg_sq=at, exp_avg_scale=at, exp_avg_sq_scale=at, numel=0,
+                                            param_type=nv.TYPE_F32, grad_type=nv.TYPE_F32, state_bits=bits))
+    size = nv.nvfp4_tensor_plan_bytes(array, 1)
+    image = torch.empty(size, dtype=torch.uint8)
+    chunks = nv.nvfp4_tensor_plan(array, 1, image.data_ptr(), size)
+    control = torch.cat([torch.ones(2, dtype=torch.float64).view(torch.int32), torch.zeros(4, dtype=torch.int32)]).cuda()
+    table = image.cuda()
+    for _ in range(2):
+        nv.nvfp4_adamw(table, chunks, bits, control, 1e-3, None, 0.5, 0.25, 1e-8, 0)
+    assert control[4:].tolist() == [2, 0, 0, 0] and control[:4].view(torch.float64).tolist() == [0.25, 0.0625]
+    assert (memory == 3).all()
