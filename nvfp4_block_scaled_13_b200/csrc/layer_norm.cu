@@ -1035,6 +1035,9 @@ bool shape_ok(int64_t rows, int64_t cols) {
 
 nvfp4_status launched() { return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
+// Threads of a CTA, at most; and forward, where a row has some lanes of a warp.
+constexpr int kMostThreads = 512, kLaneThreads = 128;
+
 // How rows are given to threads.
 struct Cut {
     int elements;   // of a thread; 0: by norm_long_kernel and its like
@@ -1053,15 +1056,15 @@ Cut cut_rows(int64_t cols, int size, bool aligned, bool congruent, bool backward
     const int64_t need = cols;
     if (!congruent) return {0, 0, 0, 1, 1, false};
     // backward one CTA an SM, so that few partial rows are left
-    const int threads = backward ? 512 : 128;
+    const int threads = backward ? kMostThreads : kLaneThreads;
     if (need <= 64) return {8, 8, threads, 8, 1, shifted};
     if (need <= 128) return {8, 16, threads, 16, 1, shifted};
     if (need <= 256) return {8, 32, threads, 32, 1, shifted};
     if (need <= 512) return {16, 32, threads, 32, 1, shifted};
     for (int cluster = 1; cluster <= 8; cluster *= 2) {
         const int64_t row = (need + 512 * cluster - 1) / (512 * cluster) * 32;   // 16 elements a thread
-        if (row <= 512) {
-            const int groups = backward && row <= 128 ? static_cast<int>(512 / row) : 1;
+        if (row <= kMostThreads) {
+            const int groups = backward && row <= 128 ? static_cast<int>(kMostThreads / row) : 1;
             return {16, cluster > 1 ? kCluster : groups > 1 ? kRows : kCta, static_cast<int>(row) * groups, static_cast<int>(row), cluster, shifted};
         }
     }
@@ -1115,22 +1118,24 @@ nvfp4_status launch(void (*kernel)(Args...), dim3 grid, int threads, int cluster
     return NVFP4_ERR_CUDA;
 }
 
-// Lets `kernel` have `bytes` of dynamic shared memory; without asking it may have 48 KiB with the
-// static arrays, which are below 8 KiB.
-template <auto kernel>
-bool allow_smem(size_t bytes) {
-    if (bytes <= 40 * 1024) return true;
+// Lets `kernel` have MOST bytes of dynamic shared memory, the most that any of its plans asks for:
+// threads that get here at once set the same value. Without asking it may have 48 KiB with the static
+// arrays, which are below 8 KiB.
+template <auto kernel, size_t MOST>
+bool allow_smem() {
+    static_assert(MOST <= (227 - 8) * 1024, "more than a CTA can have");
+    if (MOST <= 40 * 1024) return true;
     constexpr int kMaxDevices = 64;
-    static std::atomic<size_t> allowed[kMaxDevices];
+    static std::atomic<bool> allowed[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
-    if (dev < kMaxDevices && allowed[dev].load(std::memory_order_acquire) >= bytes) return true;
+    if (dev < kMaxDevices && allowed[dev].load(std::memory_order_acquire)) return true;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(bytes)) != cudaSuccess) {
+                             static_cast<int>(MOST)) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
-    if (dev < kMaxDevices) allowed[dev].store(bytes, std::memory_order_release);
+    if (dev < kMaxDevices) allowed[dev].store(true, std::memory_order_release);
     return true;
 }
 
@@ -1143,8 +1148,9 @@ nvfp4_status clear_amax(uint32_t* amax, int64_t grid, cudaStream_t stream) {
 template <typename T, int N, int LANES, bool SHIFTED>
 nvfp4_status launch_group(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
     constexpr auto kernel = norm_group_kernel<T, N, LANES, SHIFTED>;
-    const size_t smem = size_t(kForwardStages) * N * sizeof(T) * cut.threads;
-    if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
+    constexpr size_t kOfThread = size_t(kForwardStages) * N * sizeof(T);
+    const size_t smem = kOfThread * cut.threads;
+    if (!allow_smem<kernel, kOfThread * (LANES > 0 ? kLaneThreads : kMostThreads)>()) return NVFP4_ERR_CUDA;
     const int64_t parts = parts_of(cut, a.rows, int64_t(sm_count()) * resident(forward_registers(N), cut.threads), sizeof(T));
     if (clear_amax(a.amax, parts * cut.cluster, stream) != NVFP4_OK) return NVFP4_ERR_CUDA;
     return launch<NormArgs>(kernel, dim3(static_cast<unsigned>(parts * cut.cluster)), cut.threads, cut.cluster, smem,
@@ -1155,7 +1161,7 @@ template <typename T, int Q, int K, int WARPS, bool SHIFTED>
 nvfp4_status launch_norm(const NormArgs& a, cudaStream_t stream) {
     constexpr auto kernel = norm_kernel<T, Q, K, WARPS, SHIFTED>;
     constexpr size_t smem = size_t(16) * Q * 512 * kWideStages<T, Q> + size_t(WARPS) * 32 * Q * kUnit<T> * 8;
-    if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
+    if (!allow_smem<kernel, smem>()) return NVFP4_ERR_CUDA;
     constexpr int64_t unit = 16 / sizeof(T);
     const int64_t ctas = sm_count() * kWideCtas<T, Q>, room = !SHIFTED || ctas % unit == 0 ? ctas : std::max(unit, ctas / unit * unit);
     const int64_t grid = std::min(a.rows, room);
@@ -1213,8 +1219,9 @@ nvfp4_status run_norm(const NormArgs& a, const Cut& cut, cudaStream_t stream) {
 template <typename T, int N, int LANES, bool SHIFTED>
 nvfp4_status launch_grad(const NormGradArgs& a, const Cut& cut, cudaStream_t stream) {
     constexpr auto kernel = norm_grad_kernel<T, N, LANES, SHIFTED>;
-    const size_t smem = size_t(kBackwardStages) * 2 * N * sizeof(T) * cut.threads + (LANES > 0 ? size_t(4) * N * LANES : 0);
-    if (!allow_smem<kernel>(smem)) return NVFP4_ERR_CUDA;
+    constexpr size_t kOfThread = size_t(kBackwardStages) * 2 * N * sizeof(T), kWeight = LANES > 0 ? size_t(4) * N * LANES : 0;
+    const size_t smem = kOfThread * cut.threads + kWeight;
+    if (!allow_smem<kernel, kOfThread * kMostThreads + kWeight>()) return NVFP4_ERR_CUDA;
     return launch<NormGradArgs>(kernel, dim3(static_cast<unsigned>(a.parts * cut.cluster)), cut.threads, cut.cluster, smem,
                                       false, stream, a);
 }
