@@ -267,11 +267,20 @@ def _layer_norm_function():
     return _LayerNorm
 
 
+def _has_tangent(*tensors):
+    """Whether one of them is dual (forward-mode differentiation)."""
+    forward_ad = _torch.autograd.forward_ad
+    if forward_ad._current_level < 0:   # not inside a dual level: the usual case, at the price of one look
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, with_amax=False):
     """y, or (y, amax): layer norm with autograd through x, weight and bias. The amax [1] is that
-    of y's quantization (``fakequant_ste(y, amax_values=amax)``, ``quantize_for_gemm``)."""
+    of y's quantization (``fakequant_ste(y, amax_values=amax)``, ``quantize_for_gemm``). Derivatives
+    are those of the backward pass: forward-mode ones are refused, as in ``fakequant_ste``."""
     torch = _torch or _load_torch()
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+    if (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))) or _has_tangent(x, weight, bias):
         return _layer_norm_function().apply(x, weight, bias, eps, with_amax)
     r = layer_norm_forward(x, weight, bias, eps, False, with_amax)
     return (r.y, r.amax) if with_amax else r.y
