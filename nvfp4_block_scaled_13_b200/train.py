@@ -5,7 +5,11 @@ with the states in 32 bits or in 8.
 
 ``nvfp4_*`` mirror the C ABI one to one; the wrappers allocate with torch and check shapes,
 types and devices. Tensors are CUDA, contiguous and on one device, which need not be the current
-one; the work goes to ``stream``, or to the current stream of the tensors' device.
+one; the work goes to ``stream``, or to the current stream of the tensors' device. A ``stream`` that is
+not the current one must be ordered behind it (``stream.wait_stream``), because inputs come from there and
+outputs are allocated there, and the current one behind ``stream`` before it uses the outputs.
+Memory of the inputs and outputs is held until the work is done, that of a list or plan as long as its
+caller keeps it: keep it until then.
 """
 from __future__ import annotations
 
@@ -198,7 +202,7 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, with_stats=
         if status:
             _check(status, "nvfp4_layer_norm")
         if stream is not None:
-            _lend(stream, y, mean, rstd, top)
+            _lend(stream, x, weight, bias, y, mean, rstd, top)
     return Normed(y, mean, rstd, top)
 
 
@@ -235,7 +239,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, with_weight=True, with_bias=T
         if status:
             _check(status, "nvfp4_layer_norm_backward")
         if stream is not None:
-            _lend(stream, dx, dweight, dbias, work)
+            _lend(stream, dy, x, weight, mean, rstd, dx, dweight, dbias, work)
     return dx, dweight, dbias
 
 
@@ -316,7 +320,7 @@ class AdamWPlan(GradientList):
     moment's root. ``amax`` [count] is written by every ``adamw`` (None without ``with_amax``)."""
 
     def steps(self) -> int:
-        """Steps taken so far (waits for the GPU)."""
+        """Steps taken so far (waits for the current stream)."""
         return int(self.control[4].item())
 
     def set_steps(self, steps: int):
@@ -449,17 +453,19 @@ def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
     an FP32 [1] factor of the gradients, as ``grad_norm`` gives it."""
     if not isinstance(plan, AdamWPlan):
         raise ValueError("adamw: needs a plan of adamw_plan")
-    lr_device = None
+    lr_tensor = None
     if isinstance(lr, _torch.Tensor):
         _same(lr, plan.control, (1,), "lr", _torch.float32)
-        lr, lr_device = 0.0, lr.data_ptr()
+        lr, lr_tensor = 0.0, lr
     if scale is not None:
         _same(scale, plan.control, (1,), "scale", _torch.float32)
-        scale = scale.data_ptr()
     with _on(plan.device):
-        status = load().nvfp4_adamw(plan.table_ptr, plan.chunks, plan.state_bits, plan.control_ptr, float(lr), lr_device, plan.betas[0],
-                                    plan.betas[1], plan.eps, plan.seed, scale, plan.amax_ptr, plan.count, _raw(stream, plan.device))
+        status = load().nvfp4_adamw(plan.table_ptr, plan.chunks, plan.state_bits, plan.control_ptr, float(lr),
+                                    None if lr_tensor is None else lr_tensor.data_ptr(), plan.betas[0], plan.betas[1], plan.eps, plan.seed,
+                                    None if scale is None else scale.data_ptr(), plan.amax_ptr, plan.count, _raw(stream, plan.device))
         if status:
             _check(status, "nvfp4_adamw")
+        if stream is not None:
+            _lend(stream, plan.control, lr_tensor, scale)
     if plan.versioned:
         _torch.autograd.graph.increment_version(plan.versioned)

@@ -35,3 +35,45 @@ def test_forward_mode_derivatives_are_refused(gpu, which, grad):
                       lambda f: torch.func.grad(lambda x: f(x).sum())(args[0])):
         with pytest.raises(RuntimeError):
             transform(lambda x: nv.layer_norm(x, *args[1:]))
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+def test_inputs_are_held_for_a_side_stream(gpu, as_number):
+    """An input that its caller drops while a side stream still has to read it keeps its memory."""
+    n = 1 << 20
+    plan = nv.adamw_plan([torch.zeros(64, device="cuda")], [torch.ones(64, device="cuda")])
+    x = torch.randn(n // 64, 64, device="cuda")
+    w, b = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
+    r = nv.layer_norm_forward(x, w, b)
+    want = (r.y.clone(), *(t.clone() for t in nv.layer_norm_backward(x, x, w, r.mean, r.rstd)))
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_number else side
+
+    def forward(x, w, b):
+        return nv.layer_norm_forward(x, w, b, stream=stream).y
+
+    def backward(dy, x, w, mean, rstd):
+        return nv.layer_norm_backward(dy, x, w, mean, rstd, stream=stream)
+
+    def step(lr, scale):
+        nv.adamw(plan, lr, scale, stream=stream)
+
+    for call, inputs in ((forward, (x, w, b)), (backward, (x, x, w, r.mean, r.rstd)),
+                         (step, (torch.full((1,), 1e-3, device="cuda"), torch.ones(1, device="cuda")))):
+        given = [t.clone() for t in inputs]
+        at = {t.data_ptr() for t in given}
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                                 # about 10 ms in front of the call
+        got = call(*given)
+        sizes = [t.numel() for t in given]
+        given.clear()
+        new = [torch.full((k,), 7.0, device="cuda") for k in sizes for _ in range(2)]
+        assert not at & {t.data_ptr() for t in new}, call.__name__
+        torch.cuda.synchronize()
+        del new
+        if call is forward:
+            assert torch.equal(got, want[0])
+        elif call is backward:
+            assert all(torch.equal(p, q) for p, q in zip(got, want[1:]))
+    assert plan.steps() == 1 and torch.allclose(plan.params[0], torch.full((64,), -1e-3, device="cuda"))
