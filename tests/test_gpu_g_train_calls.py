@@ -42,6 +42,7 @@ def test_inputs_are_held_for_a_side_stream(gpu, as_number):
     """An input that its caller drops while a side stream still has to read it keeps its memory."""
     n = 1 << 20
     plan = nv.adamw_plan([torch.zeros(64, device="cuda")], [torch.ones(64, device="cuda")])
+    nv.adamw(plan, 0.0, torch.full((1,), float("nan"), device="cuda"))    # no step: it loads the kernel, which may outlast the delay below
     x = torch.randn(n // 64, 64, device="cuda")
     w, b = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
     r = nv.layer_norm_forward(x, w, b)
@@ -64,7 +65,7 @@ def test_inputs_are_held_for_a_side_stream(gpu, as_number):
         at = {t.data_ptr() for t in given}
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            torch.cuda._sleep(20_000_000)                                 # about 10 ms in front of the call
+            torch.cuda._sleep(200_000_000)                                # about 100 ms in front of the call
         got = call(*given)
         sizes = [t.numel() for t in given]
         given.clear()
