@@ -319,6 +319,13 @@ class AdamWPlan(GradientList):
     ``state(i)`` gives them as views. With 8-bit states ``exp_avg_sq`` holds codes of the second
     moment's root. ``amax`` [count] is written by every ``adamw`` (None without ``with_amax``)."""
 
+    def check_gradients(self):
+        """Refuses a step on gradients that are no longer the parameters' own."""
+        for p, g in self.own_gradients:
+            if p.grad is not g:
+                raise ValueError("nvfp4: a parameter's .grad is no longer the gradient that the plan was made with: clear gradients in "
+                                 "place (zero_grad(set_to_none=False)), or make a new plan")
+
     def steps(self) -> int:
         """Steps taken so far (waits for the current stream)."""
         return int(self.control[4].item())
@@ -372,7 +379,9 @@ def gradient_list(grads) -> GradientList:
 def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=0.01, betas=(0.9, 0.999),
                eps: float = 1e-8, seed: int = 0, step: int = 0, with_amax=False) -> AdamWPlan:
     """AdamW over `params` (BF16 or FP32) with the gradients in `grads`, which keep their memory
-    from step to step (assign them to ``p.grad`` and clear them in place).
+    from step to step (assign them to ``p.grad`` and clear them in place). Where a parameter's ``.grad``
+    is the given gradient, ``adamw`` and ``grad_norm`` refuse the plan once it has been replaced, as by
+    ``zero_grad()``, which sets it to None; other gradients are read where they were.
 
     ``state_bits``: 32, or 8 (E4M3 with a power-of-two scale for each 32 elements). ``masters``: an
     FP32 master of every BF16 parameter; without one a BF16 parameter is rounded stochastically.
@@ -418,6 +427,7 @@ def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=
             records.append(record)
         plan = AdamWPlan(grads, device, records)
         plan.params, plan.offsets, plan.numels = params, offsets, [p.numel() for p in params]
+        plan.own_gradients = [(p, g) for p, g in zip(params, grads) if p.is_leaf and p.grad is g]
         plan.versioned = [p for p in params if p.requires_grad or p.grad_fn is not None]
         plan.state_bits, plan.betas, plan.eps, plan.seed = state_bits, (float(betas[0]), float(betas[1])), float(eps), seed
         plan.master, plan.exp_avg, plan.exp_avg_sq = master, flat["exp_avg"], flat["exp_avg_sq"]
@@ -434,6 +444,8 @@ def grad_norm(grads: GradientList, max_norm: float = math.inf, stream=None):
     ``adamw`` leaves everything as it is."""
     if not isinstance(grads, GradientList):
         raise ValueError("grad_norm: needs a list of gradient_list, or a plan of adamw_plan")
+    if isinstance(grads, AdamWPlan):
+        grads.check_gradients()
     device = grads.device
     with _on(device):
         norm = _torch.empty(1, dtype=_torch.float32, device=device)
@@ -453,6 +465,7 @@ def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
     an FP32 [1] factor of the gradients, as ``grad_norm`` gives it."""
     if not isinstance(plan, AdamWPlan):
         raise ValueError("adamw: needs a plan of adamw_plan")
+    plan.check_gradients()
     lr_tensor = None
     if isinstance(lr, _torch.Tensor):
         _same(lr, plan.control, (1,), "lr", _torch.float32)

@@ -78,3 +78,35 @@ def test_inputs_are_held_for_a_side_stream(gpu, as_number):
         elif call is backward:
             assert all(torch.equal(p, q) for p, q in zip(got, want[1:]))
     assert plan.steps() == 1 and torch.allclose(plan.params[0], torch.full((64,), -1e-3, device="cuda"))
+
+
+def test_a_replaced_gradient_is_refused(gpu):
+    """zero_grad() sets .grad to None and the next backward allocates another: the plan's would be applied again."""
+    w = torch.nn.Parameter(torch.randn(64, device="cuda"))
+    free = torch.zeros(64, device="cuda")                                # its gradient is nobody's .grad
+    loss = lambda: (w * w).sum()  # noqa: E731
+    loss().backward()
+    plan = nv.adamw_plan([w, free], [w.grad, torch.ones(64, device="cuda")])
+    optimizer = torch.optim.SGD([w], lr=0.0)
+
+    def step():
+        _, scale = nv.grad_norm(plan, 1.0)
+        nv.adamw(plan, 1e-3, scale)
+
+    step()
+    optimizer.zero_grad(set_to_none=False)
+    loss().backward()                                                     # accumulates in place
+    step()
+    assert plan.steps() == 2
+    kept, before = w.grad, w.detach().clone()
+    optimizer.zero_grad()
+    for again in (False, True):
+        if again:
+            loss().backward()
+        for call in (lambda: nv.adamw(plan, 1e-3), lambda: nv.grad_norm(plan, 1.0)):
+            with pytest.raises(ValueError, match="grad"):
+                call()
+    assert plan.steps() == 2 and torch.equal(w.detach(), before)
+    w.grad = kept
+    step()
+    assert plan.steps() == 3
