@@ -428,7 +428,8 @@ def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=
         plan = AdamWPlan(grads, device, records)
         plan.params, plan.offsets, plan.numels = params, offsets, [p.numel() for p in params]
         plan.own_gradients = [(p, g) for p, g in zip(params, grads) if p.is_leaf and p.grad is g]
-        plan.versioned = [p for p in params if p.requires_grad or p.grad_fn is not None]
+        # every parameter's version, whether it requires a gradient or not: views share their base's
+        plan.versioned = list({id(b): b for b in (p if p._base is None else p._base for p in params)}.values())
         plan.state_bits, plan.betas, plan.eps, plan.seed = state_bits, (float(betas[0]), float(betas[1])), float(eps), seed
         plan.master, plan.exp_avg, plan.exp_avg_sq = master, flat["exp_avg"], flat["exp_avg_sq"]
         plan.exp_avg_scale, plan.exp_avg_sq_scale = flat.get("exp_avg_scale"), flat.get("exp_avg_sq_scale")
@@ -460,9 +461,10 @@ def grad_norm(grads: GradientList, max_norm: float = math.inf, stream=None):
 
 
 def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
-    """One AdamW step, in place (autograd's graphs that saved a parameter notice). ``lr``: a number, or an FP32 [1] tensor that the kernel reads (a
-    captured call then follows it; the count of steps is kept on the device anyway). ``scale``:
-    an FP32 [1] factor of the gradients, as ``grad_norm`` gives it."""
+    """One AdamW step, in place: autograd's graphs that saved a parameter notice (not at a replay of
+    a captured call). ``lr``: a number, or an FP32 [1] tensor that the kernel reads (a captured call
+    then follows it; the count of steps is kept on the device anyway). ``scale``: an FP32 [1] factor
+    of the gradients, as ``grad_norm`` gives it."""
     if not isinstance(plan, AdamWPlan):
         raise ValueError("adamw: needs a plan of adamw_plan")
     plan.check_gradients()
@@ -480,5 +482,4 @@ def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
             _check(status, "nvfp4_adamw")
         if stream is not None:
             _lend(stream, plan.control, lr_tensor, scale)
-    if plan.versioned:
-        _torch.autograd.graph.increment_version(plan.versioned)
+    _torch.autograd.graph.increment_version(plan.versioned)

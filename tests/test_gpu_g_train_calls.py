@@ -110,3 +110,27 @@ def test_a_replaced_gradient_is_refused(gpu):
     w.grad = kept
     step()
     assert plan.steps() == 3
+
+
+@pytest.mark.parametrize("kind", ["plain", "later", "view", "view of a leaf", "inference"])
+def test_every_graph_that_saved_a_parameter_notices_the_step(gpu, kind):
+    """A parameter that requires no gradient itself, or requires one only after the plan was made."""
+    x = torch.randn(64, device="cuda", requires_grad=True)
+    if kind == "inference":
+        with torch.inference_mode():
+            p = torch.randn(64, device="cuda")
+        nv.adamw(nv.adamw_plan([p], [torch.ones(64, device="cuda")]), 1e-3)   # has no version to count
+        return
+    flat = torch.randn(128, device="cuda", requires_grad=kind == "view of a leaf")
+    p = flat[64:] if kind.startswith("view") else torch.randn(64, device="cuda")
+    other = torch.randn(64, device="cuda")
+    plan = nv.adamw_plan([p, other], [torch.ones(64, device="cuda") for _ in range(2)])
+    if kind == "later":
+        p.requires_grad_()
+    y = (p * x).sum() + (other * x).sum()
+    nv.adamw(plan, 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    fresh = (p * x).sum() + (other * x).sum()
+    fresh.backward()
+    assert torch.equal(x.grad, p.detach() + other)
