@@ -1176,8 +1176,8 @@ nvfp4_status launch_wide(const NormArgs& a, int need, cudaStream_t stream) {
     constexpr int S = SHIFTED;
     const int units = (need + WARPS * 256 - 1) / (WARPS * 256);
     if constexpr (sizeof(T) == 4) {
-        if (FROM <= 2 && units <= 2) return launch_norm<T, 4, 2 - S, WARPS, SHIFTED>(a, stream);
-        if (FROM <= 4 && units <= 4) return launch_norm<T, 8, 4 - S, WARPS, SHIFTED>(a, stream);
+        if constexpr (FROM <= 2) if (units <= 2) return launch_norm<T, 4, 2 - S, WARPS, SHIFTED>(a, stream);
+        if constexpr (FROM <= 4) if (units <= 4) return launch_norm<T, 8, 4 - S, WARPS, SHIFTED>(a, stream);
         return launch_norm<T, 16, 8 - S, WARPS, SHIFTED>(a, stream);
     } else {
         if constexpr (FROM <= 2) if (units == 2) return launch_norm<T, 2, 1 - S, WARPS, SHIFTED>(a, stream);
