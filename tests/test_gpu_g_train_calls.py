@@ -1,5 +1,8 @@
 """How the training-step operators are called: derivatives, streams, gradients and versions."""
 import gc
+import subprocess
+import sys
+import textwrap
 
 import pytest
 import torch
@@ -134,3 +137,63 @@ def test_every_graph_that_saved_a_parameter_notices_the_step(gpu, kind):
     fresh = (p * x).sum() + (other * x).sum()
     fresh.backward()
     assert torch.equal(x.grad, p.detach() + other)
+
+
+COLD = textwrap.dedent("""
+    import torch
+
+    import nvfp4_block_scaled_13_b200 as nv
+
+    x = torch.randn(300, 1029, device="cuda").bfloat16()
+    w = torch.ones(1029, device="cuda").bfloat16()
+    dy = (x * 1e-3).roll(1, 0).contiguous()
+    p, g = torch.ones(5000, device="cuda"), torch.full((5000,), 0.5, device="cuda")
+    plan = nv.adamw_plan([p], [g], state_bits=8, with_amax=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = nv.layer_norm_forward(x, w, w, with_amax=True)
+        back = nv.layer_norm_backward(dy, x, w, r.mean, r.rstd)
+        norm, scale = nv.grad_norm(plan, 1.0)
+        nv.adamw(plan, 1e-3, scale)
+    for _ in range(3):
+        graph.replay()
+    want = nv.layer_norm_forward(x, w, w, with_amax=True)
+    assert all(torch.equal(a, b) for a, b in zip(r, want))
+    assert all(torch.equal(a, b) for a, b in zip(back, nv.layer_norm_backward(dy, x, w, want.mean, want.rstd)))
+    assert plan.steps() == 3 and abs(norm.item() - 0.5 * 5000 ** 0.5) < 1e-4 and plan.amax.item() == p.max().item() < 1
+    print("done")
+""")
+
+
+def test_first_calls_in_a_process_are_captured(gpu):
+    """Nothing has run before the capture: kernels are loaded and their shared memory allowed within it."""
+    r = subprocess.run([sys.executable, "-c", COLD], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "done", r.stderr[-2000:]
+
+
+def test_two_plans_and_lists_on_two_streams(gpu):
+    """Steps and norms that overlap on the GPU, each with a plan of its own, give what they give alone."""
+    def made(k):
+        gen = torch.Generator(device="cuda").manual_seed(k)
+        params = [torch.randn(n, device="cuda", generator=gen).bfloat16() for n in (70001, 4096, 33)]
+        grads = [torch.randn(p.numel(), device="cuda", generator=gen) for p in params]
+        return nv.adamw_plan(params, grads, state_bits=8, with_amax=True, seed=k)
+
+    def step(plan, stream=None):
+        _, scale = nv.grad_norm(plan, 1.0, stream=stream)
+        nv.adamw(plan, 1e-3, scale, stream=stream)
+
+    alone, both = [made(k) for k in range(2)], [made(k) for k in range(2)]
+    for _ in range(4):
+        for plan in alone:
+            step(plan)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for _ in range(4):
+        for plan, stream in zip(both, streams):
+            step(plan, stream)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        for p, q in zip((*a.params, a.exp_avg, a.exp_avg_sq, a.exp_avg_scale, a.exp_avg_sq_scale, a.amax),
+                        (*b.params, b.exp_avg, b.exp_avg_sq, b.exp_avg_scale, b.exp_avg_sq_scale, b.amax)):
+            assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
