@@ -42,7 +42,8 @@ typedef enum {
  *           nvfp4_amax. NaN if a y is NaN; 0 for an empty tensor                      (out)
  * The variance is the mean square distance from the mean, taken from the row held on chip, so
  * a large mean cancels nothing. Every pointer needs its element's alignment only; x and y are
- * best at the same place within 16 bytes. cols >= 1 and rows >= 0 (else NVFP4_ERR_SHAPE), eps
+ * best at the same place within 16 bytes (else rows are read three times by the element, about five
+ * times as slow). cols >= 1 and rows >= 0 (else NVFP4_ERR_SHAPE), eps
  * finite and >= 0 (else NVFP4_ERR_VALUE). One kernel, one read of x (rows of more
  * than 65536 columns, and operands that start at different places within 16 bytes, are read
  * again from L2), after a zero-fill of amax where more than one CTA runs. */
@@ -161,6 +162,7 @@ typedef struct {
  * Random words. Element i of a tensor (k = first + i), t - 1 steps taken, mod 2^32:
  *   word = mix((k >> 3) ^ mix(seed + 0x9E3779B9 * (t - 1))) + (k & 7) * 0x9E3779B9
  *   mix(a): a ^= a >> 16; a *= 0x85EBCA6B; a ^= a >> 13; a *= 0xC2B2AE35; a ^= a >> 16
+ *   (the 32-bit finalizer of MurmurHash3, a bijection)
  * Its high half is added to the 16 bits that a BF16 parameter drops; its low half to the upper
  * 16 of the 20 bits that a code of u drops.
  *   plan, chunks  as for nvfp4_grad_norm, of a list of optimizer tensors             (in)
@@ -175,8 +177,8 @@ typedef struct {
  *              does not take place: only amax is written                             (in)
  *   amax       NULL, or [count] float: max |param| of each tensor as stored, the amax of its next
  *              fake-quantization; zero-filled first in stream order; 0 for an empty tensor (out)
- *   count      number of tensors of the plan, read where amax is given (another number: nothing is
- *              done)
+ *   count      number of tensors of the plan, read where amax is given (another number: amax is
+ *              zero-filled and nothing else is done)
  * Calls on one control block or one list must not overlap on the GPU. One kernel. */
 NVFP4_API nvfp4_status nvfp4_adamw(const void* plan, int64_t chunks, int32_t state_bits,
                                    nvfp4_adamw_control* control, float lr, const float* lr_device, double beta1, double beta2, float eps, uint32_t seed,

@@ -6,9 +6,10 @@
 // 8-bit states took 420 us, against 377).
 //
 // An element costs, with BF16 gradients, 28 bytes with an FP32 master and 32-bit states: memory
-// bounds that step (168 M elements: 798 us, 90% of the copy bandwidth). A BF16 parameter with 8-bit
-// states costs 10.125 bytes and 49 instructions: there the issue slots bound it (200 M elements:
-// 367 us, 84%). Hence paired (f32x2) arithmetic, three-operand maxima, addition of random bits in place
+// bounds that step (168 M elements: 802 us, 89% of the copy bandwidth). A BF16 parameter with 8-bit
+// states costs 10.125 bytes and 49 instructions: there the issue slots bound it (200 M elements in
+// eight tensors: 362 us, 85%; 201 M in fourteen whose gradients differ in scale, the states of three
+// plans in turn: 410 us, 76%). Hence paired (f32x2) arithmetic, three-operand maxima, addition of random bits in place
 // of a comparison, and rare cases (zero codes, NaN) behind one test for eight elements.
 //
 // The step's arithmetic is binary32 with its fused operations stated one by one, so with 32-bit
@@ -36,9 +37,9 @@ constexpr int kTile = kThreads * 8;        // elements of one pass of a CTA: eig
 constexpr uint32_t kMagic = 0x4E56504Cu;
 constexpr uint32_t kGolden = 0x9E3779B9u;
 // CTAs of an SM in a step. 8-bit states need 80 registers: with 64, for four CTAs, they spill (556 us
-// for 200 M elements in place of 445 at that stage). 32-bit states fit into 64, but four CTAs stream
-// from too many places at once: 168 M elements with masters took 835 us with four, 798 with three
-// and 863 with two.
+// for 200 M elements in place of 445 at that stage). 32-bit states spill a little at 80 (36 bytes
+// stored, 44 loaded) and more at 64 (48 and 304), and four CTAs stream from more places at once: 168 M
+// elements with masters took 835 us with four, 798 with three and 863 with two.
 constexpr int kStepCtas = 3;
 constexpr int kNormCtas = 4;
 // Ring of each CTA (8-bit states), as much as three CTAs can have: 200 M elements took 464 us with
@@ -187,6 +188,7 @@ __device__ __forceinline__ uint2 encode_stochastic(const float2 (&u)[4], float i
     return make_uint2(w[0], w[1]);
 }
 
+// The 32-bit finalizer of MurmurHash3 (Austin Appleby, public domain), a bijection.
 __device__ __forceinline__ uint32_t mix(uint32_t a) {
     a ^= a >> 16;
     a *= 0x85EBCA6Bu;
@@ -250,7 +252,9 @@ struct StepArgs {
 // rounded to 4 bits, and the update is added to a parameter that it changes in its last bits. A v
 // that counts as 0 takes up to 2^-63 from u, which an eps of at least kLeastEps hides (2^-27 of the
 // denominator); and the reciprocal of a denominator above 2^126 is 0. Any other eps, 0 among them, takes
-// the rounded root and quotient in their place (ROUNDED below).
+// the rounded root and quotient in their place (ROUNDED below), in an instance of its own, because one
+// branch for both spilled in the usual one: 201 M BF16 weights take 353 us with the approximations and
+// 592 without.
 constexpr float kLeastEps = 0x1p-36f, kMostEps = 0x1p100f;
 __device__ __forceinline__ float approximate_root(float v) {
     float r;

@@ -3,8 +3,9 @@
 // Forward, per row of x: mean = S x / C, var = S (x - mean)^2 / C, rstd = (var + eps)^-1/2,
 // y = (x - mean) rstd w + b. Backward, with xh = (x - mean) rstd and h = dy w:
 // dx = rstd (h - S h / C - xh S(h xh) / C), dw = S_rows dy xh, db = S_rows dy.
-// Both are bound by memory: 4 bytes an element forward and 6 backward in BF16 (8192 x 4096: 25 us with
-// the amax, where a copy of the same size takes 22; 42 us backward, 73% of the copy bandwidth).
+// Both are bound by memory: 4 bytes an element forward and 6 backward in BF16 (8192 x 4096 on the
+// device: 25.7 us with the amax, where a copy of the same size takes 22.3; 41.9 us backward, 73% of the
+// copy bandwidth. FP32, 4096 x 4096: 24.7 and 36.3 us, 83% and 85%).
 //
 // A row belongs to a group of threads: 8, 16 or 32 lanes of a warp (no barrier), some warps of a CTA,
 // or a cluster of CTAs that exchange their sums through shared memory. A thread holds its share of the row in registers from the loads to the result, so x (and dy) are
@@ -320,7 +321,7 @@ constexpr int kBackwardStages = 3;
 // Registers of a thread, and with them the CTAs that an SM holds (each of its four quarters has
 // 16384 registers).
 constexpr int forward_registers(int elements) { return elements == 16 ? 80 : 64; }
-constexpr int kBackwardRegisters = 128;
+constexpr int kBackwardRegisters = 128;   // shifted rows in groups of a CTA (kRows) spill 104 to 116 bytes beside it
 constexpr int resident(int registers, int threads) {
     return std::max(1, std::min(32, 16384 / (registers * 32) * 4 / (threads / 32)));
 }
@@ -494,8 +495,10 @@ __global__ void __maxnreg__(forward_registers(N)) norm_group_kernel(const __grid
 // gridDim.x-th row, which gives all of them one head.
 template <int WARPS>
 constexpr int kWideThreads = 16 / WARPS * WARPS * 32;   // whole row groups
+// Rows in the ring: four where a row is so short that two are little to have on the way (BF16 of 257 to
+// 512 columns; 30000 x 257 takes 15.7 us, 16384 x 512 9.6 us).
 template <typename T, int Q>
-constexpr int kWideStages = Q <= 2 ? 4 : sizeof(T) == 2 || Q <= 8 ? 2 : 1;   // rows in the ring
+constexpr int kWideStages = Q <= 2 ? 4 : sizeof(T) == 2 || Q <= 8 ? 2 : 1;
 template <typename T, int Q>
 constexpr int kWideCtas = Q * 16 <= 32 ? 2 : 1;                           // CTAs of an SM
 
@@ -650,8 +653,10 @@ __device__ __forceinline__ uint32_t stored_magnitude(float v, bf16) {
 }
 __device__ __forceinline__ uint32_t stored_magnitude(float v, float) { return magnitude(v); }
 
-// Rows too long for one CTA's registers, and operands whose rows start at different places within
-// 16 bytes: three passes by the element, the later two from L1 or L2.
+// Rows of over 65536 columns, and operands whose rows start at different places within 16 bytes: three
+// passes by the element, the later two from L1 or L2. The second costs a factor of five: 8192 x 4096
+// in BF16 with x one element past a boundary and y on one takes 141 us (25.7 where both lie on one),
+// 245 backward (41.9).
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     __shared__ float scratch[2][32];
