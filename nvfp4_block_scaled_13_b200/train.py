@@ -322,7 +322,8 @@ class AdamWPlan(GradientList):
     def check_gradients(self):
         """Refuses a step on gradients that are no longer the parameters' own."""
         for p, g in self.own_gradients:
-            if p.grad is not g:
+            now = p.grad
+            if now is not g and (now is None or now.data_ptr() != g.data_ptr() or now.dtype != g.dtype or not now.is_contiguous()):
                 raise ValueError("nvfp4: a parameter's .grad is no longer the gradient that the plan was made with: clear gradients in "
                                  "place (zero_grad(set_to_none=False)), or make a new plan")
 

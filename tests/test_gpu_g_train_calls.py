@@ -197,3 +197,15 @@ def test_two_plans_and_lists_on_two_streams(gpu):
         for p, q in zip((*a.params, a.exp_avg, a.exp_avg_sq, a.exp_avg_scale, a.exp_avg_sq_scale, a.amax),
                         (*b.params, b.exp_avg, b.exp_avg_sq, b.exp_avg_scale, b.exp_avg_sq_scale, b.amax)):
             assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
+def test_another_tensor_over_the_same_gradient_is_accepted(gpu):
+    w = torch.nn.Parameter(torch.ones(6, 8, device="cuda"))
+    w.grad = torch.ones(6, 8, device="cuda")
+    plan = nv.adamw_plan([w], [w.grad])
+    w.grad = w.grad.detach()
+    nv.adamw(plan, 1e-3)
+    assert plan.steps() == 1
+    w.grad = plan.grads[0].clone()
+    with pytest.raises(ValueError, match="grad"):
+        nv.adamw(plan, 1e-3)
