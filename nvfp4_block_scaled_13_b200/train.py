@@ -300,6 +300,7 @@ class GradientList:
     def __init__(self, grads, device, records):
         torch = _torch
         self.grads, self.device, self.count = grads, device, len(records)
+        self.held = [g.detach() for g in grads]   # their memory, which the table points to, whatever becomes of the tensors
         array = (OptTensor * max(1, len(records)))(*records)
         size = nvfp4_tensor_plan_bytes(array, len(records))
         if size < 0:
@@ -318,6 +319,12 @@ class AdamWPlan(GradientList):
     buffers; those of tensor i start at ``offsets[i]`` (scales at ``offsets[i] // 32``), and
     ``state(i)`` gives them as views. With 8-bit states ``exp_avg_sq`` holds codes of the second
     moment's root. ``amax`` [count] is written by every ``adamw`` (None without ``with_amax``)."""
+
+    def check_parameters(self):
+        """Refuses a step on memory that is no longer the parameters'."""
+        if list(map(_torch.Tensor.data_ptr, self.params)) != self.addresses:
+            raise ValueError("nvfp4: a parameter's memory is no longer the one that the plan was made with (as after .to() or an assignment "
+                             "to .data): make a new plan")
 
     def check_gradients(self):
         """Refuses a step on gradients that are no longer the parameters' own."""
@@ -382,7 +389,8 @@ def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=
     """AdamW over `params` (BF16 or FP32) with the gradients in `grads`, which keep their memory
     from step to step (assign them to ``p.grad`` and clear them in place). Where a parameter's ``.grad``
     is the given gradient, ``adamw`` and ``grad_norm`` refuse the plan once it has been replaced, as by
-    ``zero_grad()``, which sets it to None; other gradients are read where they were.
+    ``zero_grad()``, which sets it to None; other gradients are read where they were. A parameter that
+    was given other memory, as by ``module.to()``, is refused likewise.
 
     ``state_bits``: 32, or 8 (E4M3 with a power-of-two scale for each 32 elements). ``masters``: an
     FP32 master of every BF16 parameter; without one a BF16 parameter is rounded stochastically.
@@ -428,6 +436,8 @@ def adamw_plan(params, grads, state_bits: int = 32, masters=False, weight_decay=
             records.append(record)
         plan = AdamWPlan(grads, device, records)
         plan.params, plan.offsets, plan.numels = params, offsets, [p.numel() for p in params]
+        plan.held += [p.detach() for p in params]
+        plan.addresses = [p.data_ptr() for p in params]
         plan.own_gradients = [(p, g) for p, g in zip(params, grads) if p.is_leaf and p.grad is g]
         # every parameter's version, whether it requires a gradient or not: views share their base's
         plan.versioned = list({id(b): b for b in (p if p._base is None else p._base for p in params)}.values())
@@ -468,6 +478,7 @@ def adamw(plan: AdamWPlan, lr, scale=None, stream=None):
     of the gradients, as ``grad_norm`` gives it."""
     if not isinstance(plan, AdamWPlan):
         raise ValueError("adamw: needs a plan of adamw_plan")
+    plan.check_parameters()
     plan.check_gradients()
     lr_tensor = None
     if isinstance(lr, _torch.Tensor):

@@ -209,3 +209,26 @@ def test_another_tensor_over_the_same_gradient_is_accepted(gpu):
     w.grad = plan.grads[0].clone()
     with pytest.raises(ValueError, match="grad"):
         nv.adamw(plan, 1e-3)
+
+
+@pytest.mark.parametrize("how", ["to", "data"])
+def test_a_parameter_with_other_memory_is_refused(gpu, how):
+    """The plan's table still points to the old memory, which must not have been given to somebody else."""
+    module = torch.nn.Linear(64, 1 << 14, bias=False, device="cuda")
+    w = module.weight
+    g = torch.ones_like(w)
+    plan = nv.adamw_plan([w], [g])
+    grads = nv.gradient_list([g])
+    nv.adamw(plan, 1e-3)
+    at = {w.data_ptr(), g.data_ptr()}
+    if how == "to":
+        module.to(torch.bfloat16)
+    else:
+        w.data = w.data.clone()
+    g.data = torch.zeros(0, device="cuda")
+    assert w is module.weight
+    new = [torch.zeros(64 << 14, device="cuda") for _ in range(3)]
+    with pytest.raises(ValueError, match="memory"):
+        nv.adamw(plan, 1e-3)
+    assert not at & {t.data_ptr() for t in new} and grads.held[0].data_ptr() in at
+    assert plan.steps() == 1
