@@ -251,10 +251,10 @@ struct StepArgs {
 // approximations (relative errors of at most 2^-23 each; a v below 2^-126 counts as 0). u is then
 // rounded to 4 bits, and the update is added to a parameter that it changes in its last bits. A v
 // that counts as 0 takes up to 2^-63 from u, which an eps of at least kLeastEps hides (2^-27 of the
-// denominator); and the reciprocal of a denominator above 2^126 is 0. Any other eps, 0 among them, takes
-// the rounded root and quotient in their place (ROUNDED below), in an instance of its own, because one
-// branch for both spilled in the usual one: 201 M BF16 weights take 353 us with the approximations and
-// 592 without.
+// denominator, times 1 / sqrt(1 - beta2^t), which is at most 32 with beta2 = 0.999); and the reciprocal of
+// a denominator above 2^126 is 0. Any other eps, 0 among them, takes the rounded root and quotient in
+// their place (ROUNDED below), in an instance of its own, because one branch for both spilled in the usual
+// one: 201 M BF16 weights take 353 us with the approximations and 592 without.
 constexpr float kLeastEps = 0x1p-36f, kMostEps = 0x1p100f;
 __device__ __forceinline__ float approximate_root(float v) {
     float r;
